@@ -56,8 +56,10 @@ typedef enum {
   MOE_ERR_BAD_FORCED_ID = -4, /* a forced id was out of range or repeated within a token */
   MOE_ERR_TIMEOUT = -5,       /* a device-side wait gave up */
   MOE_ERR_CUDA = -6,          /* a CUDA runtime call failed */
-  MOE_ERR_INDEX = -7          /* MOE_DEBUG builds only: a kernel's index check failed (an internal
+  MOE_ERR_INDEX = -7,         /* MOE_DEBUG builds only: a kernel's index check failed (an internal
                                  error of the library; the access was kept inside its buffer) */
+  MOE_ERR_BAD_PAGE = -8       /* a token's sequence, position or page was outside the page table or
+                                 the cache */
 } moe_status;
 
 /* MOE_E2M1: 4-bit weights (OCP E2M1 codes: sign bit 3, magnitudes 0, 0.5, 1, 1.5, 2, 3, 4,
@@ -237,6 +239,104 @@ moe_status moe_get_status(void* ws, moe_stream_t stream);
  *   Allocates nothing (no cudaMalloc, no cudaFree). */
 moe_status moe_route_noalloc(const void* x, moe_dtype x_dtype, int T, const moe_layer* layer, int k,
                              int32_t* ids_out, float* w_out, moe_stream_t stream);
+
+/* ---- the decode step between two expert layers: paged cache, attention, norms -----------------
+ *
+ * A Kolibri-style decoder layer is attention and then the expert layer on one residual stream,
+ * 40 layers with a 513-token sliding window and every fifth with full context (page "We Ported
+ * Aleph Alpha's Kolibri to a MacBook. Our Own Gate Said No.", section "The gate").  The calls
+ * below are what a decode step needs around moe_forward and the two projections.  They follow
+ * the conventions at the top; device-side errors go to the status record of the workspace they
+ * are given. */
+
+/* A paged key-value cache: n_pages pages of page_size tokens, each token with n_kv_heads keys and
+ * values of head_dim elements.
+ *   k, v          [n_pages, n_kv_heads, page_size, head_dim]  bf16, or E4M3 codes
+ *   k_exp, v_exp  [n_pages, n_kv_heads, page_size] uint8 (E4M3 only, else NULL): a row's values
+ *                 are its codes times 2^(exp - 127)
+ * Position p of sequence s lives in row p % page_size of page page_table[s, p / page_size], of a
+ * page_table [n_seqs, max_pages] int32 on the device that the caller fills as it hands out pages
+ * (entries beyond a sequence's length are not read).
+ * dtype MOE_BF16 or MOE_E4M3; page_size a multiple of 16, up to 4096; head_dim a multiple of 16, up
+ * to 256; n_kv_heads up to 1024; all pointers 16-byte aligned. */
+typedef struct {
+  int n_pages, page_size, n_kv_heads, head_dim;
+  moe_dtype dtype;
+  void* k;
+  void* v;
+  uint8_t* k_exp;
+  uint8_t* v_exp;
+} moe_kv_cache;
+
+/* Writes T tokens' keys and values into the cache.
+ *   k, v      T rows of [n_kv_heads, head_dim], bf16 or fp32 (kv_dtype), the rows k_stride and
+ *             v_stride elements apart (a fused projection's output is taken as it lies); both a
+ *             multiple of 16 bytes
+ *   seq, pos  [T] int32: each token's sequence and position; seq NULL: token t is sequence t's.
+ *             A negative position skips the token.  Two tokens at one place leave either's row.
+ * bf16 cache: values rounded to nearest even.  E4M3 cache: a row's exponent is the smallest power
+ * of two (2^-127 at least) that brings its largest magnitude to 448 at most, and its codes are the
+ * scaled values rounded to nearest even: scaling by a power of two is exact, so each value is
+ * rounded once and moe_kv_read returns it without another rounding.
+ * A sequence outside [0, n_seqs), a position past the page table or a page outside [0, n_pages)
+ * writes nothing and records MOE_ERR_BAD_PAGE in ws (any workspace of this library). */
+moe_status moe_kv_write(const moe_kv_cache* cache, const void* k, const void* v, moe_dtype kv_dtype, int64_t k_stride,
+                        int64_t v_stride, int T, const int32_t* seq, const int32_t* pos, const int32_t* page_table,
+                        int n_seqs, int max_pages, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Reads T tokens' keys and values back: k_out, v_out [T, n_kv_heads, head_dim] bf16 or fp32
+ * (out_dtype), token t from sequence seq[t] (NULL: t) and position pos[t].  A skipped or refused
+ * token (as for moe_kv_write) reads as zeros. */
+moe_status moe_kv_read(const moe_kv_cache* cache, int T, const int32_t* seq, const int32_t* pos,
+                       const int32_t* page_table, int n_seqs, int max_pages, void* k_out, void* v_out,
+                       moe_dtype out_dtype, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Bytes of workspace moe_attn_decode needs for up to B sequences of n_heads query heads on this
+ * cache's shape (host only; 0 for a shape it refuses). */
+size_t moe_attn_workspace_bytes(const moe_kv_cache* cache, int n_heads, int B);
+
+/* Clears an attention workspace's status record and join counters.  Call once after allocating
+ * it, and again after MOE_ERR_TIMEOUT.  An attention workspace serves moe_attn_decode calls of any
+ * size that fits, one at a time, and no moe_forward (which would overwrite the counters).
+ * Asynchronous on `stream`. */
+moe_status moe_attn_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Attention of one new token a sequence over the paged cache.  Query head h reads kv head
+ * h / (n_heads / n_kv_heads); for sequence b with n = lens[b] cached tokens (the new one among
+ * them: moe_kv_write first) and j from max(0, n - window) (window 0: from 0) to n - 1,
+ *   out[b,h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[b,h].k_j - max),
+ *   lse[b,h] = log sum_j exp(scale q[b,h].k_j)
+ *   q           B rows of [n_heads, head_dim] bf16, q_stride elements apart (a multiple of 8)
+ *   lens        [B] int32 on the device; sequence b is row b of page_table [B, max_pages]
+ *   out         [B, n_heads, head_dim] bf16
+ *   lse         [B, n_heads] fp32 or NULL: joins this result with another part of the context
+ * n <= 0 gives zeros and an lse of -infinity.  n beyond the page table is cut to it, and a page
+ * outside [0, n_pages) is left out as if masked; both record MOE_ERR_BAD_PAGE.  What lies in the
+ * cache outside the window (NaN and infinity included) has no effect.  Scores, sums and the
+ * accumulators are fp32; the results do not depend on the order in which CTAs finish.
+ * n_heads a multiple of n_kv_heads, up to 1024; B up to 65536. */
+moe_status moe_attn_decode(const moe_kv_cache* cache, const void* q, int64_t q_stride, int n_heads, int B,
+                           const int32_t* lens, const int32_t* page_table, int max_pages, float scale, int window,
+                           void* out, float* lse, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* What stands between two blocks on the residual stream, in one pass over [T, d]:
+ *   z  = y * rsqrt(mean(y^2) + eps) * w_post     (w_post NULL: z = y)
+ *   z  = z * gate                                (gate NULL: no gate)
+ *   r' = residual + alpha * z                    (y NULL: r' = residual)
+ *   x  = r' * rsqrt(mean(r'^2) + eps) * w_pre    (the next block's input)
+ *   y             [T, d] bf16 or fp32 (y_dtype): the block's output, or NULL
+ *   w_post, w_pre [d] fp32
+ *   gate          rows of d elements, bf16 or fp32 (gate_dtype), gate_stride elements apart (a
+ *                 multiple of 8; 0: one row for all tokens), or NULL
+ *   residual      [T, d] bf16 or fp32 (r_dtype); residual_out likewise (may be residual itself)
+ *   x             [T, d] bf16 or fp32 (x_dtype), or NULL (then w_pre is not read)
+ * All sums are fp32; r' and x are each rounded once, x from the fp32 r'.  residual_out may be NULL
+ * when y is (the residual then stays as it is).  d a multiple of 8, up to 16384; y, residual,
+ * w_post, w_pre, gate, x 16-byte aligned; alpha finite, eps >= 0. */
+moe_status moe_block_norm(const void* y, moe_dtype y_dtype, const float* w_post, const void* gate,
+                          moe_dtype gate_dtype, int64_t gate_stride, float alpha, const void* residual,
+                          void* residual_out, moe_dtype r_dtype, const float* w_pre, void* x, moe_dtype x_dtype, int T,
+                          int d, float eps, moe_stream_t stream);
 
 /* Exercises the device-side timeout path: launches one CTA whose wait on a barrier can never
  * complete; the wait gives up after timeout_us (<= 1 s) and records MOE_ERR_TIMEOUT in the

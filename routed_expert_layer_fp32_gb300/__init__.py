@@ -3,3 +3,4 @@ with a thin ctypes binding (`binding`)."""
 from . import binding  # noqa: F401
 from .binding import (GraphedForward, GraphedStack, Layer, MoeError, dispatch, e4m3_encode, forward,  # noqa: F401
                       forward_stack, get_status, route, workspace, workspace_bytes)
+from .decoder import KVCache, attn_decode, attn_workspace, block_norm, kv_read, kv_write  # noqa: F401

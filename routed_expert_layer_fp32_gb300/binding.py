@@ -20,13 +20,15 @@ LAYOUT_ROWS, LAYOUT_TILED = 0, 1
 BIAS_SCORE, BIAS_SELECT = 0, 1
 PATH_AUTO, PATH_STREAM, PATH_TC = 0, 1, 2
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED", -3: "MOE_ERR_WORKSPACE",
-          -4: "MOE_ERR_BAD_FORCED_ID", -5: "MOE_ERR_TIMEOUT", -6: "MOE_ERR_CUDA", -7: "MOE_ERR_INDEX"}
+          -4: "MOE_ERR_BAD_FORCED_ID", -5: "MOE_ERR_TIMEOUT", -6: "MOE_ERR_CUDA", -7: "MOE_ERR_INDEX",
+          -8: "MOE_ERR_BAD_PAGE"}
 
 # every entry point include/libmoe.h declares
 EXPORTS = ("moe_workspace_bytes", "moe_workspace_init", "moe_route", "moe_dispatch", "moe_forward",
            "moe_forward_stack", "moe_forward_traced", "moe_forward_stack_traced", "moe_get_status",
            "moe_status_string", "moe_e4m3_encode", "moe_route_noalloc", "moe_selftest_wait_timeout",
-           "moe_pack_weights")
+           "moe_pack_weights", "moe_kv_write", "moe_kv_read", "moe_attn_workspace_bytes", "moe_attn_workspace_init",
+           "moe_attn_decode", "moe_block_norm")
 TRACE_POINTS = 9
 TRACE_STAGES = ("router", "select", "dispatch", "act_quant", "gate_up", "h_quant", "down", "combine")
 
@@ -90,9 +92,18 @@ def load(path: str):
     L.moe_route_noalloc.argtypes = [vp, i32, i32, vp, i32, vp, vp, vp]
     L.moe_selftest_wait_timeout.argtypes = [vp, sz, u32, vp]
     L.moe_pack_weights.argtypes = [vp, vp, vp, vp, vp, vp]
+    f32 = ctypes.c_float
+    L.moe_kv_write.argtypes = [vp, vp, vp, i32, i64, i64, i32, vp, vp, vp, i32, i32, vp, sz, vp]
+    L.moe_kv_read.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, vp, i32, vp, sz, vp]
+    L.moe_attn_workspace_bytes.argtypes = [vp, i32, i32]
+    L.moe_attn_workspace_bytes.restype = sz
+    L.moe_attn_workspace_init.argtypes = [vp, sz, vp]
+    L.moe_attn_decode.argtypes = [vp, vp, i64, i32, i32, vp, vp, i32, f32, i32, vp, vp, vp, sz, vp]
+    L.moe_block_norm.argtypes = [vp, i32, vp, vp, i32, i64, f32, vp, vp, i32, vp, vp, i32, i32, i32, f32, vp]
     for f in ("moe_workspace_init", "moe_route", "moe_dispatch", "moe_forward", "moe_forward_stack",
               "moe_forward_traced", "moe_forward_stack_traced", "moe_get_status", "moe_e4m3_encode",
-              "moe_route_noalloc", "moe_selftest_wait_timeout", "moe_pack_weights"):
+              "moe_route_noalloc", "moe_selftest_wait_timeout", "moe_pack_weights", "moe_kv_write", "moe_kv_read",
+              "moe_attn_workspace_init", "moe_attn_decode", "moe_block_norm"):
         getattr(L, f).restype = i32
     return L
 

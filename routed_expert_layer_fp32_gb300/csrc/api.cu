@@ -329,6 +329,7 @@ moe_status moe_get_status(void* ws, moe_stream_t stream) {
   if (cudaMemset(ws, 0, sizeof(DevStatus)) != cudaSuccess) return MOE_ERR_CUDA;
   if (h.flags & kFlagIndex) return MOE_ERR_INDEX;
   if (h.flags & kFlagBadForced) return MOE_ERR_BAD_FORCED_ID;
+  if (h.flags & kFlagBadPage) return MOE_ERR_BAD_PAGE;
   if (h.flags & kFlagTimeout) return MOE_ERR_TIMEOUT;
   return MOE_OK;
 }
@@ -342,6 +343,7 @@ const char* moe_status_string(moe_status status) {
     case MOE_ERR_BAD_FORCED_ID: return "a forced expert id was out of range or repeated within a token";
     case MOE_ERR_TIMEOUT: return "a device-side wait timed out";
     case MOE_ERR_CUDA: return "a CUDA runtime call failed";
+    case MOE_ERR_BAD_PAGE: return "a token's sequence, position or page was outside the page table or the cache";
     case MOE_ERR_INDEX: return "an index check of a MOE_DEBUG build failed (an internal error)";
   }
   return "unknown status";

@@ -16,7 +16,7 @@ constexpr int kMaxTokens = 1 << 20;
 
 // Device-side status record (first bytes of the workspace).
 struct DevStatus {
-  int flags;        // bit 0: bad forced id, bit 1: timeout
+  int flags;        // bit 0: bad forced id, bit 1: timeout, bit 2: index check, bit 3: bad page
   int bad_forced;   // number of rejected forced slots
   int timeout_site; // where a bounded wait gave up (0 = none)
   int dispatch_ticket;  // decode router: selecting CTAs done, the last one dispatches; 0 between launches
@@ -26,6 +26,7 @@ struct DevStatus {
 static_assert(sizeof(DevStatus) == 768, "DevStatus is three 256-byte blocks");
 constexpr int kFlagBadForced = 1;
 constexpr int kFlagTimeout = 2;
+constexpr int kFlagBadPage = 8;
 
 // One work tile of a grouped GEMM: rows [row0, row0 + nrows) of group `group`
 // (group == n_experts is the shared expert).
