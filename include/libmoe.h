@@ -258,7 +258,7 @@ moe_status moe_route_noalloc(const void* x, moe_dtype x_dtype, int T, const moe_
  * page_table [n_seqs, max_pages] int32 on the device that the caller fills as it hands out pages
  * (entries beyond a sequence's length are not read).
  * dtype MOE_BF16 or MOE_E4M3; page_size a multiple of 16, up to 4096; head_dim a multiple of 16, up
- * to 256; n_kv_heads up to 1024; all pointers 16-byte aligned. */
+ * to 256; n_kv_heads up to 1024; n_pages * n_kv_heads * page_size below 2^31; all pointers 16-byte aligned. */
 typedef struct {
   int n_pages, page_size, n_kv_heads, head_dim;
   moe_dtype dtype;
@@ -314,7 +314,8 @@ moe_status moe_attn_workspace_init(void* ws, size_t ws_bytes, moe_stream_t strea
  * outside [0, n_pages) is left out as if masked; both record MOE_ERR_BAD_PAGE.  What lies in the
  * cache outside the window (NaN and infinity included) has no effect.  Scores, sums and the
  * accumulators are fp32; the results do not depend on the order in which CTAs finish.
- * n_heads a multiple of n_kv_heads, up to 1024; B up to 65536. */
+ * n_heads a multiple of n_kv_heads, up to 1024; B up to 65536; max_pages * page_size up to 2^28, and
+ * (max_pages * page_size / 32 + 1) * B * n_kv_heads * ceil(n_heads / n_kv_heads / 4) below 2^31. */
 moe_status moe_attn_decode(const moe_kv_cache* cache, const void* q, int64_t q_stride, int n_heads, int B,
                            const int32_t* lens, const int32_t* page_table, int max_pages, float scale, int window,
                            void* out, float* lse, void* ws, size_t ws_bytes, moe_stream_t stream);

@@ -23,6 +23,7 @@ moe_status check_cache(const moe_kv_cache* c) {
   if (c->dtype == MOE_E4M3 && (!c->k_exp || !c->v_exp || !aligned16(c->k_exp) || !aligned16(c->v_exp)))
     return MOE_ERR_INVALID_ARG;
   if (c->page_size % 16 != 0 || c->page_size > kMaxPageSize) return MOE_ERR_UNSUPPORTED;
+  if (int64_t(c->n_pages) * c->n_kv_heads >= (int64_t(1) << 31) / c->page_size) return MOE_ERR_UNSUPPORTED;
   if (c->head_dim % 16 != 0 || c->head_dim > kMaxHeadDim || c->n_kv_heads > kMaxHeads) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -128,8 +129,11 @@ moe_status moe_attn_decode(const moe_kv_cache* cache, const void* q, int64_t q_s
   if (!lens || !aligned4(lens) || !out || !aligned16(out) || !aligned4(lse)) return MOE_ERR_INVALID_ARG;
   rc = check_table(page_table, B, max_pages);
   if (rc != MOE_OK) return rc;
-  // positions are 32-bit
-  if (int64_t(max_pages) * cache->page_size > (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
+  // positions and the tiles of a call are counted in 32 bits (a tile is of 32 tokens and 4 heads at least)
+  const int64_t room = int64_t(max_pages) * cache->page_size, group = n_heads / cache->n_kv_heads;
+  if (room > (int64_t(1) << 28) ||
+      (room / 32 + 1) * B * cache->n_kv_heads >= (int64_t(1) << 31) / ((group + 3) / 4))
+    return MOE_ERR_UNSUPPORTED;
   if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
   AttnArgs a;
   a.cache = to_dev(cache);

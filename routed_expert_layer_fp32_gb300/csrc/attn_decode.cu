@@ -5,10 +5,8 @@
 //
 // with the running maximum m, the sum and the accumulator in fp32.  In an E4M3 cache key j is
 // 2^a_j times its codes and value j is 2^c_j times its codes: 2^a_j multiplies the score, and the
-// weight of value j's codes is w_j = p_j 2^c_j.  There m is the running maximum of t_j + c_j, so
-// that no w_j is above 1 and the largest is close to it: w_j is then rounded to fp16 without
-// losing the rows that matter, however the rows' sizes differ.  In a bf16 cache w_j = p_j, rounded
-// to bf16 (a product's operands have one type); the sum takes p_j before the rounding.
+// weight of value j's codes is w_j = p_j 2^c_j; there m is the maximum of t_j + c_j, so that no w_j
+// is above 1 and the largest is close to it, however the rows' sizes differ.
 //
 // What bounds it is reading the cache: 2 * group operations an element (group = query heads a kv
 // head), against about 290 a byte for the tensor cores.  So the kernel is built around keeping
@@ -22,68 +20,97 @@
 // accumulator) in the workspace, and the CTA that writes the last of them (a counter a segment,
 // back to 0 afterwards) joins them in CTA order, so the result does not depend on timing.
 //
-// In a CTA, one warp is the producer: it looks up pages and starts the tiles' TMA copies into a
-// ring of shared-memory stages (about 190 KB of them in flight a SM).  The other warps form groups
-// that take the CTA's tiles in turn; a warp has kPerWarp tokens of each of its group's tiles and
-// its own m, sum and accumulator, which are joined once a segment through shared memory.  Copies
-// of the next segments go on meanwhile.
+// In a CTA, a warp is the producer: it looks up pages and starts the tiles' TMA copies into a ring of
+// shared-memory stages.  Another lays the next segments' queries out as operands.  Eight warps
+// compute, in groups that take the tiles in turn; a warp has kPerWarp tokens of each of its group's
+// tiles and its own m, sum and accumulator, and at a segment's end leaves them in shared memory and
+// goes on.  Four warps add the eight results up, write the output or the partial result, and join
+// partial results.  So neither the copies nor the products wait for a segment's end (with all of that
+// in the eight warps, a segment cost 3.5 us next to 3 us of products at 513 tokens).  A stage belongs
+// to one group: a barrier's wait tells only the parity of the phase, so whoever waits for a stage has
+// to have seen each of its phases.
 //
-// The products are warp MMAs (m16n8k16) with the tokens (scores) and the value elements (output)
-// on the M side and the query heads on the N side, so that eight heads, not sixteen, are the unit
-// that a small group is padded to; a tcgen05 product has at least 64 rows on M and its scores
-// would have to travel through TMEM.  Keys and values reach the registers by ldmatrix from the
-// swizzled tiles, the values transposed; E4M3 codes become fp16 on the way (exact), the queries
-// fp16 after scaling by a power of two (exact but for elements 2^-38 below a head's largest).
+// Starting a copy holds a warp up for 100 to 200 cycles, which is enough time for two warps to fall
+// behind the memory with the 2 KB copies of 16-token pages if they compute anything else there: no
+// division a tile, and each lane has its own copy of every tile worked out beforehand.
+//
+// The products are warp MMAs with the tokens (scores) and the value elements (output) on the M
+// side and the query heads on the N side, so that eight columns are the unit that a small group is
+// padded to; a tcgen05 product has at least 64 rows on M, and its scores would have to travel
+// through TMEM.  Keys and values reach the registers by ldmatrix from the swizzled tiles, the
+// values transposed.
 #include "decoder.cuh"
 #include "tcgen05.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;  // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kWarps = 8;      // compute
+constexpr int kProducers = 2;  // start copies
+constexpr int kQueryWarp = kWarps + kProducers;
+constexpr int kEndWarp = kWarps + 4;  // the first of those that end segments
+constexpr int kEndThreads = 128;
+constexpr int kThreads = kEndWarp * 32 + kEndThreads;
+// Registers a thread of the four warpgroups (compute twice, producers, segment ends); the launch gives
+// each 128, and the shares add up to that.
+constexpr int kComputeRegs = 168, kProducerRegs = 72, kEndRegs = 104;
+static_assert(2 * kComputeRegs + kProducerRegs + kEndRegs <= 4 * (65536 / kThreads), "registers");
+constexpr size_t kSmemLimit = 227 * 1024;
 constexpr int kMaxCtas = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinExp = -100;  // least value exponent that enters m: keeps the sum inside fp32's range
 static_assert(kMaxCtas <= kAttnTickets, "a counter a CTA");
 
-template <bool kE4M3_, int kDim_, int kBlocks_>
+template <bool kE4M3_, int kDim_, int kHeads_>
 struct Shape {
   static constexpr bool kE4M3 = kE4M3_;
-  static constexpr int kDim = kDim_;        // head_dim rounded up to 64, 128 or 256 (copies fill with zeros)
-  static constexpr int kBlocks = kBlocks_;  // blocks of eight query heads
-  static constexpr int kHeads = 8 * kBlocks;
+  static constexpr int kDim = kDim_;      // head_dim rounded up to 64, 128 or 256 (copies fill with zeros)
+  static constexpr int kHeads = kHeads_;  // query heads of a segment
   static constexpr int kRow = kDim * (kE4M3 ? 1 : 2);       // bytes
   static constexpr int kSpan = kRow < 128 ? kRow : 128;     // bytes of a row in one swizzled copy
   static constexpr int kSpans = kRow / kSpan;
   static constexpr int kSpanElems = kDim / kSpans;
-  // 32 KB stages (16 KB for the narrowest rows): 32 tokens a warp where a stage has room for that
-  static constexpr int kPerWarp = kRow <= 128 ? 32 : 16;
-  static constexpr int kGroupWarps = kRow <= 256 ? 4 : 2;
+  // 32 KB stages (16 KB for the narrowest rows), 32 tokens a warp; 16 where the accumulators of two
+  // blocks of eight heads, or of wide rows, fill the registers
+  static constexpr int kPerWarp = !kE4M3 && kHeads * kDim > 1024 ? 16 : 32;
+  static constexpr int kTokens = kRow <= 128 ? 128 : 128 * 128 / kRow;
+  static constexpr int kGroupWarps = kTokens / kPerWarp;
   static constexpr int kGroups = kWarps / kGroupWarps;
-  static constexpr int kTokens = kPerWarp * kGroupWarps;
   static constexpr int kTile = kTokens * kRow;
   static constexpr int kExps = kE4M3 ? 2 * kTokens : 0;     // the keys' and the values' exponents
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = 192 * 1024 / kStage;
-  static constexpr int kOutLd = kDim + 4;                    // row of the join buffer: no bank conflicts
+  // the queries of kSlots segments as B operands: kQueryRegs registers a lane, and a factor a head
+  static constexpr int kQueryRegs = kE4M3 ? kDim / 32 * (kHeads / 4) * 2 : kDim / 16 * (kHeads / 8) * 2;
+  static constexpr int kQueries = kQueryRegs * 128 + kHeads * 4;
+  static constexpr int kSlots = 4;
+  // the join buffer: kPassDim elements of every warp's accumulators at a time, rows padded against
+  // bank conflicts (two heads a lane group in the bf16 form, one in the E4M3 form)
+  static constexpr int kPassDim = kDim < 1024 / kHeads ? kDim : 1024 / kHeads;
+  static constexpr int kPasses = kDim / kPassDim;
+  static constexpr int kJoinRow = kPassDim + (kE4M3 ? 8 : 4);
+  static constexpr int kJoinWarp = kHeads * kJoinRow;        // floats
   static constexpr int kSlot = kHeads * (kDim + 2);          // floats of a partial result
+  static constexpr int kMaxStages = 16;
   struct Control {
-    uint64_t full[kStages], empty[kStages];
-    uint32_t valid[kStages];  // a bit for each 16 tokens of the tile: copied
+    uint64_t full[kMaxStages], empty[kMaxStages], q_full[kSlots], q_empty[kSlots], join_full, join_empty, merge_full;
+    uint32_t valid[kMaxStages];  // a bit for each 16 tokens of the tile: copied
     int abort;
-    int b0, last;
-    long long off0, scan[kWarps + 1];
+    int b0, off0, last, scan[kThreads / 32];
     float m[kWarps][kHeads], sum[kWarps][kHeads];
-    float total_m[kHeads], total_sum[kHeads];
   };
-  // layout: stages, exponents, join buffer, control
+  // layout: stages, exponents, queries, join buffer, control; 1 KB to align the stages
+  static constexpr size_t kFixed = size_t(kSlots) * kQueries + size_t(kWarps) * kJoinWarp * 4 + sizeof(Control) + 1024;
+  static constexpr int kRoom = int((kSmemLimit - kFixed) / (kStage + kExps));
+  static constexpr int kStages = kRoom < 192 * 1024 / kStage ? kRoom : 192 * 1024 / kStage;
   static constexpr size_t kExpsAt = size_t(kStages) * kStage;
-  static constexpr size_t kOutAt = kExpsAt + size_t(kStages) * kExps;
-  static constexpr size_t kControlAt = kOutAt + size_t(kHeads) * kOutLd * 4;
-  static constexpr size_t kSmem = kControlAt + sizeof(Control) + 1024;  // and room to align the stages
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static constexpr size_t kQueriesAt = kExpsAt + size_t(kStages) * kExps;
+  static constexpr size_t kJoinAt = kQueriesAt + size_t(kSlots) * kQueries;
+  static constexpr size_t kControlAt = kJoinAt + size_t(kWarps) * kJoinWarp * 4;
+  static constexpr size_t kSmem = kControlAt + sizeof(Control) + 1024;
+  static_assert(kSmem <= kSmemLimit && kStages >= 4 && kStages <= kMaxStages, "shared memory");
+  static_assert(kGroupWarps >= 1 && kWarps % kGroupWarps == 0, "groups");
+  static_assert(kQueries % 16 == 0 && kJoinAt % 16 == 0 && kControlAt % 16 == 0, "alignment");
 };
 
 // ------------------------------------------------------------------ instructions ------------
@@ -105,41 +132,35 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t r) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(r));
   return t;
 }
-template <bool kHalf>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  if constexpr (kHalf)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_bf16_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ float exp2_fast(float x) {  // exp2(-inf) = 0; relative error 2^-22
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two E4M3 codes (low half of `codes`) as fp16.
-__device__ __forceinline__ uint32_t half2_of_codes(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(codes), __NV_E4M3);
-  return uint32_t(h.x) | uint32_t(h.y) << 16;
+// Two E4M3 codes (low half of `codes`) as fp32.
+__device__ __forceinline__ float2 float2_of_codes(uint32_t codes) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(codes), __NV_E4M3)));
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 p = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
-                                            uint32_t bar) {
+// Rows from `row` on (a box of a map made by cache_map), from element x on.
+__device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, int x, int row, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(row), "r"(0), "r"(smem_u32(bar))
       : "memory");
+}
+// mbar_wait, without its look at the clock where the phase is over already.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
+  return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort);
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 __device__ __forceinline__ float max_over_rows(float v) {  // over the lanes that share lane % 4
 #pragma unroll
@@ -151,7 +172,15 @@ __device__ __forceinline__ float sum_over_rows(float v) {
   for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ void consumers_sync() { named_bar_sync(1, kWarps * 32); }
+__device__ __forceinline__ void end_sync() { named_bar_sync(1, kEndThreads); }  // of the warps that end segments
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 // ----------------------------------------------------------------------- the split ----------
 
@@ -175,19 +204,18 @@ template <typename S>
 struct Walk {
   int b, seg, tile;  // sequence, segment in it, first tile (of the segment's) that is ours
   int take;          // how many tiles are ours
-  long long pos, hi;
+  int pos, hi;       // on the line (below 2^31 tiles)
   Span span;
 
-  __device__ __forceinline__ void start(const AttnArgs& a, int segs, int b0, long long off0, long long lo,
-                                        long long hi_) {
+  __device__ __forceinline__ void start(const AttnArgs& a, int b0, int off0, int lo, int hi_) {
     pos = lo;
     hi = hi_;
     b = b0;
     if (pos >= hi) return;
     span = span_of<S>(a, b);
-    seg = int(off0 / span.tiles);
-    tile = int(off0 - (long long)seg * span.tiles);
-    take = int(min((long long)(span.tiles - tile), hi - pos));
+    seg = off0 / span.tiles;
+    tile = off0 - seg * span.tiles;
+    take = min(span.tiles - tile, hi - pos);
   }
   __device__ __forceinline__ bool done() const { return pos >= hi; }
   __device__ __forceinline__ void next(const AttnArgs& a, int segs) {
@@ -199,21 +227,565 @@ struct Walk {
       do span = span_of<S>(a, ++b);
       while (span.tiles == 0);  // pos < hi: a sequence with tiles follows
     }
-    take = int(min((long long)span.tiles, hi - pos));
+    take = min(span.tiles, hi - pos);
+  }
+  __device__ __forceinline__ bool whole() const { return take == span.tiles; }  // the segment is all ours
+  __device__ __forceinline__ bool last() const { return pos + take == hi; }
+};
+
+// The line cut into the CTAs' parts: the first `more` have one tile more than the others.
+struct Parts {
+  int each, more;
+  __device__ __forceinline__ Parts(int total, int ctas) {
+    each = ctas > 0 ? total / ctas : 0;
+    more = total - each * ctas;
+  }
+  __device__ __forceinline__ int begin(int cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ int owner(int tile) const {
+    const int wide = more * (each + 1);
+    return tile < wide ? tile / (each + 1) : more + (tile - wide) / each;
+  }
+};
+
+// ------------------------------------------------------------------------ a warp ------------
+
+// What a consumer warp needs to know of a tile.
+struct TileView {
+  uint32_t k, v;        // shared-memory addresses of the key and value tiles
+  const uint8_t* exps;  // of the keys; the values' follow kTokens further
+  int pos0;             // position of the warp's first token
+  int first, end;       // the positions that are seen
+  uint32_t valid;       // a bit for each 16 of the warp's tokens: copied
+  __device__ __forceinline__ bool seen(int r) const {
+    return (valid >> (r / 16) & 1) && pos0 + r >= first && pos0 + r < end;
+  }
+  // 0xffff a seen token: tokens r (low half) and r + 1
+  __device__ __forceinline__ uint32_t keep2(int r) const {
+    return (seen(r) ? 0xffffu : 0u) | (seen(r + 1) ? 0xffff0000u : 0u);
+  }
+};
+
+// Addresses for ldmatrix.  A tile lies in shared memory box by box (the tokens of one copy, a multiple
+// of 16), a box span by span.  A 16-byte chunk i of row r of a span lies at chunk i ^ (r % 8) of the row
+// (128-byte rows), or i ^ (r / 2 % 4) (64-byte rows).
+template <typename S>
+struct Rows {
+  uint32_t at[S::kPerWarp / 16], flip, span;
+  __device__ __forceinline__ Rows(int row, int odd_chunk, int box) {
+#pragma unroll
+    for (int i = 0; i < S::kPerWarp / 16; ++i) {
+      const int r = row + i * 16;
+      at[i] = uint32_t(r / box * box * S::kRow + r % box * S::kSpan);
+    }
+    flip = uint32_t((odd_chunk ^ (S::kSpan == 64 ? (row >> 1) & 3 : row & 7)) << 4);
+    span = uint32_t(box * S::kSpan);
+  }
+  // chunk 2 i (lanes whose odd_chunk is 1: 2 i + 1) of the lane's row, `block` blocks of 16 rows down
+  // (which leaves the swizzle as it is)
+  __device__ __forceinline__ uint32_t operator()(uint32_t tile, int block, int i) const {
+    constexpr int kPairs = S::kSpan / 32;
+    return tile + at[block] + i / kPairs * span + (uint32_t((i % kPairs) << 5) ^ flip);
+  }
+};
+
+// One warp's running result over a bf16 cache.  Scores: keys (16 tokens x 16 elements, as they lie)
+// times queries; the weights, rounded to bf16 (the type of the values: a product's operands have
+// one), go through an 8 x 8 transpose to become the B operand of values^T times weights.  Lane
+// (g, t) = (lane / 4, lane % 4) holds tokens g and g + 8 of a block, and heads 2t and 2t + 1 of a
+// block of eight.
+template <typename S>
+struct WarpBf16 {
+  static constexpr int kMT = S::kPerWarp / 16, kKS = S::kDim / 16, kNB = S::kHeads / 8;
+  uint32_t q[kKS][kNB][2];
+  float m[kNB][2], sum[kNB][2], acc[kKS][kNB][4];
+  float factor;  // scores to base-2 exponents
+  Rows<S> k_rows, v_rows;
+  int g, t;
+
+  __device__ __forceinline__ WarpBf16(int row0, int lane, int box)
+      : k_rows(row0 + (lane & 15), lane >> 4, box),
+        v_rows(row0 + (lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1, box),
+        g(lane >> 2),
+        t(lane & 3) {}
+
+  // Register [ks][nb][i] of lane (g, t): head nb * 8 + g, elements 16 ks + 8 i + 2t and the next.
+  static __device__ __forceinline__ void lay_out(uint8_t* queries, const __nv_bfloat16* q, int heads, int dim,
+                                                 float scale_log2e, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t r[kNB][kKS][2];
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb) {
+      const uint32_t* row = reinterpret_cast<const uint32_t*>(q + int64_t(nb * 8 + g) * dim) + t;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)  // head_dim is a multiple of 16
+          r[nb][ks][i] = nb * 8 + g < heads && ks * 16 < dim ? __ldg(row + ks * 8 + i * 4) : 0u;
+    }
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+      for (int ks = 0; ks < kKS; ks += 2)
+        *reinterpret_cast<uint4*>(queries + ((nb * kKS + ks) / 2 * 32 + lane) * 16) =
+            make_uint4(r[nb][ks][0], r[nb][ks][1], r[nb][ks + 1][0], r[nb][ks + 1][1]);
+    if (lane < S::kHeads) reinterpret_cast<float*>(queries + S::kQueryRegs * 128)[lane] = scale_log2e;
+  }
+
+  __device__ __forceinline__ void begin(const uint8_t* queries, int lane) {
+    factor = *reinterpret_cast<const float*>(queries + S::kQueryRegs * 128);
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb) {
+      m[nb][0] = m[nb][1] = -INFINITY;
+      sum[nb][0] = sum[nb][1] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[ks][nb][i] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ks += 2) {
+        const uint4 u = *reinterpret_cast<const uint4*>(queries + ((nb * kKS + ks) / 2 * 32 + lane) * 16);
+        q[ks][nb][0] = u.x, q[ks][nb][1] = u.y, q[ks + 1][nb][0] = u.z, q[ks + 1][nb][1] = u.w;
+      }
+    }
+  }
+
+  template <bool kWhole>  // all of the warp's tokens are seen
+  __device__ __forceinline__ void tile(const TileView& tv) {
+    float s[kMT][kNB][4];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+      float s2[kNB][4];  // two chains of products
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[mt][nb][i] = s2[nb][i] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks) {
+        uint32_t r[4];
+        ldmatrix4(k_rows(tv.k, mt, ks), r);
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb) mma_bf16_16x8x16(ks & 1 ? s2[nb] : s[mt][nb], r, q[ks][nb][0], q[ks][nb][1]);
+      }
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = (s[mt][nb][i] + s2[nb][i]) * factor;
+          s[mt][nb][i] = kWhole || tv.seen(mt * 16 + (i >> 1) * 8 + g) ? x : -INFINITY;
+        }
+    }
+    float base[kNB][2], fix[kNB][2];
+    bool moved = false;
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float top = fmaxf(s[0][nb][i], s[0][nb][2 + i]);
+#pragma unroll
+        for (int mt = 1; mt < kMT; ++mt) top = fmaxf(top, fmaxf(s[mt][nb][i], s[mt][nb][2 + i]));
+        const float now = fmaxf(m[nb][i], max_over_rows(top));
+        base[nb][i] = now == -INFINITY ? 0.0f : now;  // nothing seen yet: exp2(-inf - 0) = 0
+        fix[nb][i] = exp2_fast(m[nb][i] - base[nb][i]);
+        moved |= now != m[nb][i];
+        m[nb][i] = now;
+      }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb) {
+        sum[nb][0] *= fix[nb][0];
+        sum[nb][1] *= fix[nb][1];
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[ks][nb][i] *= fix[nb][i & 1];
+      }
+    }
+    uint32_t w[kMT][kNB][2];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float p0 = exp2_fast(s[mt][nb][2 * half] - base[nb][0]);
+          const float p1 = exp2_fast(s[mt][nb][2 * half + 1] - base[nb][1]);
+          sum[nb][0] += p0;
+          sum[nb][1] += p1;
+          w[mt][nb][half] = transpose8x8(pack_bf16x2(p0, p1));
+        }
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+      // what lies in rows that are not seen may be no number: 0 there
+      const uint32_t keep0 = kWhole ? 0u : tv.keep2(mt * 16 + 2 * t), keep1 = kWhole ? 0u : tv.keep2(mt * 16 + 8 + 2 * t);
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks) {
+        uint32_t r[4];
+        ldmatrix4_trans(v_rows(tv.v, mt, ks), r);
+        if (!kWhole) r[0] &= keep0, r[1] &= keep0, r[2] &= keep1, r[3] &= keep1;
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb) mma_bf16_16x8x16(acc[ks][nb], r, w[mt][nb][0], w[mt][nb][1]);
+      }
+    }
+  }
+
+  // m and sum [kHeads], and elements [pass * kPassDim, ...) of the accumulators [kHeads][kJoinRow]
+  __device__ __forceinline__ void publish_sums(float* m_out, float* sum_out) {
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float all = sum_over_rows(sum[nb][i]);
+        if (g == 0) {
+          m_out[nb * 8 + 2 * t + i] = m[nb][i];
+          sum_out[nb * 8 + 2 * t + i] = all;
+        }
+      }
+  }
+  template <int kPass>
+  __device__ __forceinline__ void publish(float* out, int heads) {
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int h = nb * 8 + 2 * t + i;
+        if (h >= heads) continue;  // columns without a head
+#pragma unroll
+        for (int j = 0; j < S::kPassDim / 16; ++j) {
+          out[h * S::kJoinRow + j * 16 + g] = acc[kPass * (S::kPassDim / 16) + j][nb][i];
+          out[h * S::kJoinRow + j * 16 + 8 + g] = acc[kPass * (S::kPassDim / 16) + j][nb][2 + i];
+        }
+      }
+  }
+};
+
+// One warp's running result over an E4M3 cache.  The codes go into the products as they are
+// (converting them to a wider type would cost more instructions than all the rest): E4M3 x E4M3
+// products with fp32 sums.
+//
+// A query element x of 8 significant bits, scaled by a power of two to below 2^8, is split into two
+// E4M3 numbers, hi = round(x) and lo = 32 (x - hi): both exact, unless x is below 2^-14 of its head's
+// largest (then off by at most 2^-22 of that).  A weight w is split likewise, hi + lo / 32 of 256 w,
+// which leaves the error of a bf16 rounding (2^-8).  A block of eight columns is four heads: column
+// 2h holds the hi of head h, column 2h + 1 its lo, so lane (g, t) has both products of head t and
+// adds them up.
+//
+// The smallest step of the split is 2^-22 of the largest weight, so the weights are taken relative
+// to the maximum over the warp's own 32 tokens, and the product is added to the accumulator by an
+// fp32 factor: a long row of small weights keeps its precision beside a large one.
+//
+// The values' codes: a register of ldmatrix with transpose holds elements 2g and 2g + 1 of tokens 2t
+// and 2t + 1; a byte permutation of it and the one of tokens 2t + 8 and 2t + 9 gives the four
+// tokens of one element that the A operand takes.  The weights come out of the 8 x 8 transpose of
+// (token g, token g + 8) pairs in that same order.
+template <typename S>
+struct WarpE4M3 {
+  static constexpr int kKS = S::kDim / 32, kNB = S::kHeads / 4, kMD = S::kDim / 16;
+  static_assert(S::kPerWarp == 32, "the 32 tokens of one product with the values");
+  uint32_t q[kKS][kNB][2];
+  float m[kNB], sum[kNB], factor[kNB], acc[kMD][kNB][2];
+  Rows<S> rows;
+  int g, t;
+
+  __device__ __forceinline__ WarpE4M3(int row0, int lane, int box)
+      : rows(row0 + (lane & 15), lane >> 4, box), g(lane >> 2), t(lane & 3) {}
+
+  // hi or lo codes of four query elements
+  static __device__ __forceinline__ uint32_t split4(uint2 u, float down, bool lo) {
+    const float x0 = __uint_as_float(u.x << 16) * down, x1 = __uint_as_float(u.x & 0xffff0000u) * down;
+    const float x2 = __uint_as_float(u.y << 16) * down, x3 = __uint_as_float(u.y & 0xffff0000u) * down;
+    const uint32_t h01 = e4m3_code2(x0, x1), h23 = e4m3_code2(x2, x3);
+    const float2 f01 = float2_of_codes(h01), f23 = float2_of_codes(h23);
+    const uint32_t l01 = e4m3_code2((x0 - f01.x) * 32.0f, (x1 - f01.y) * 32.0f);
+    const uint32_t l23 = e4m3_code2((x2 - f23.x) * 32.0f, (x3 - f23.y) * 32.0f);
+    return lo ? l01 | l23 << 16 : h01 | h23 << 16;
+  }
+
+  // Register [ks][nb][i] of lane (g, t): column g of block nb (head nb * 4 + g / 2, its hi or lo),
+  // elements 32 ks + 16 i + 4t and the three after.
+  static __device__ __forceinline__ void lay_out(uint8_t* queries, const __nv_bfloat16* q, int heads, int dim,
+                                                 float scale_log2e, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+    for (int nb = 0; nb < kNB; ++nb) {
+      const int h = nb * 4 + (g >> 1);
+      const uint2* row = reinterpret_cast<const uint2*>(q + int64_t(h) * dim) + t;
+      uint2 u[kKS][2];
+      float top = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          u[ks][i] = h < heads && ks * 32 + i * 16 < dim ? __ldg(row + ks * 8 + i * 4) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[ks][i].x << 16)), fabsf(__uint_as_float(u[ks][i].x & 0xffff0000u))));
+          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[ks][i].y << 16)), fabsf(__uint_as_float(u[ks][i].y & 0xffff0000u))));
+        }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // times 2^-e the largest is in [2^7, 2^8)
+      const int e = min(120, max(-100, int(__float_as_uint(top) >> 23) - 127 - 7));
+      const float down = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks)
+        *reinterpret_cast<uint2*>(queries + ((nb * kKS + ks) * 32 + lane) * 8) =
+            make_uint2(split4(u[ks][0], down, g & 1), split4(u[ks][1], down, g & 1));
+      // a query with an infinity or NaN has no finite scores
+      const float lost = top < INFINITY ? 1.0f : __uint_as_float(0x7fc00000u);
+      if (t == 0 && !(g & 1))
+        reinterpret_cast<float*>(queries + S::kQueryRegs * 128)[h] =
+            scale_log2e * (__uint_as_float(uint32_t(127 + e) << 23) * lost);
+    }
+  }
+
+  __device__ __forceinline__ void begin(const uint8_t* queries, int lane) {
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb) {
+      m[nb] = -INFINITY;
+      sum[nb] = 0.0f;
+      factor[nb] = reinterpret_cast<const float*>(queries + S::kQueryRegs * 128)[nb * 4 + t];
+#pragma unroll
+      for (int md = 0; md < kMD; ++md) acc[md][nb][0] = acc[md][nb][1] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks) {
+        const uint2 u = *reinterpret_cast<const uint2*>(queries + ((nb * kKS + ks) * 32 + lane) * 8);
+        q[ks][nb][0] = u.x, q[ks][nb][1] = u.y;
+      }
+    }
+  }
+
+  template <bool kWhole>
+  __device__ __forceinline__ void tile(const TileView& tv) {
+    float s[2][kNB][2];  // tokens g and g + 8 of both blocks, head t of each column block
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      float d[kNB][4];
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[nb][i] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < kKS; ++ks) {
+        uint32_t r[4];
+        ldmatrix4(rows(tv.k, mt, ks), r);
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb) mma_e4m3_16x8x32(d[nb], r[0], r[1], r[2], r[3], q[ks][nb][0], q[ks][nb][1]);
+      }
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb) {
+        s[mt][nb][0] = fmaf(d[nb][1], 1.0f / 32.0f, d[nb][0]);
+        s[mt][nb][1] = fmaf(d[nb][3], 1.0f / 32.0f, d[nb][2]);
+      }
+    }
+    float unit[2][2];  // 2^c of the tokens' values
+    float top[kNB];
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb) top[nb] = -INFINITY;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = mt * 16 + half * 8 + g;
+        const bool seen = kWhole || tv.seen(r);
+        const float k_unit = exp_value(tv.exps[r]);
+        const uint32_t ve = tv.exps[S::kTokens + r];
+        const float c = float(max(int(ve) - kExpBias, kMinExp));
+        unit[mt][half] = seen ? exp_value(ve) : 0.0f;
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb) {
+          float& x = s[mt][nb][half];
+          x = seen ? x * (factor[nb] * k_unit) : -INFINITY;
+          top[nb] = fmaxf(top[nb], x + c);
+        }
+      }
+    float base[kNB], now[kNB];  // the maximum over these tokens, and over all so far
+    bool moved = false;
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb) {
+      const float here = max_over_rows(top[nb]);
+      now[nb] = fmaxf(m[nb], here);
+      moved |= now[nb] != m[nb];
+      base[nb] = here == -INFINITY ? 0.0f : here;
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb) {
+        const float fix = now[nb] == -INFINITY ? 0.0f : exp2_fast(m[nb] - now[nb]);
+        m[nb] = now[nb];
+        sum[nb] *= fix;
+#pragma unroll
+        for (int md = 0; md < kMD; ++md) acc[md][nb][0] *= fix, acc[md][nb][1] *= fix;
+      }
+    }
+    uint32_t w[kNB][2];
+    float into[kNB];  // of the product, in the accumulator: 2^-8 for the 256
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb) {
+      const float f = m[nb] == -INFINITY ? 0.0f : exp2_fast(base[nb] - m[nb]);
+      float all = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const float p0 = exp2_fast(s[mt][nb][0] - base[nb]), p1 = exp2_fast(s[mt][nb][1] - base[nb]);
+        all += p0 + p1;
+        const float w0 = p0 * unit[mt][0] * 256.0f, w1 = p1 * unit[mt][1] * 256.0f;
+        const uint32_t hi = e4m3_code2(w0, w1);
+        const float2 f2 = float2_of_codes(hi);
+        const uint32_t lo = e4m3_code2((w0 - f2.x) * 32.0f, (w1 - f2.y) * 32.0f);
+        w[nb][mt] = transpose8x8(hi | lo << 16);
+      }
+      sum[nb] = fmaf(all, f, sum[nb]);
+      into[nb] = f * (1.0f / 256.0f);
+    }
+    uint32_t keep[2][2];
+    if (!kWhole) {
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) keep[mt][0] = tv.keep2(mt * 16 + 2 * t), keep[mt][1] = tv.keep2(mt * 16 + 8 + 2 * t);
+    }
+#pragma unroll
+    for (int i = 0; i < kKS; ++i) {
+      uint32_t r[2][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        ldmatrix4_trans(rows(tv.v, mt, i), r[mt]);
+        if (!kWhole) r[mt][0] &= keep[mt][0], r[mt][1] &= keep[mt][1], r[mt][2] &= keep[mt][0], r[mt][3] &= keep[mt][1];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        // element 2g of tokens 2t, 2t + 8, 2t + 1, 2t + 9 (row g of the operand), and 2g + 1 (row g + 8)
+        const uint32_t a0 = __byte_perm(r[0][2 * h], r[0][2 * h + 1], 0x6240);
+        const uint32_t a1 = __byte_perm(r[0][2 * h], r[0][2 * h + 1], 0x7351);
+        const uint32_t a2 = __byte_perm(r[1][2 * h], r[1][2 * h + 1], 0x6240);
+        const uint32_t a3 = __byte_perm(r[1][2 * h], r[1][2 * h + 1], 0x7351);
+#pragma unroll
+        for (int nb = 0; nb < kNB; ++nb) {
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma_e4m3_16x8x32(d, a0, a1, a2, a3, w[nb][0], w[nb][1]);
+          float(&o)[2] = acc[2 * i + h][nb];
+          o[0] = fmaf(fmaf(d[1], 1.0f / 32.0f, d[0]), into[nb], o[0]);
+          o[1] = fmaf(fmaf(d[3], 1.0f / 32.0f, d[2]), into[nb], o[1]);
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void publish_sums(float* m_out, float* sum_out) {
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb) {
+      const float all = sum_over_rows(sum[nb]);
+      if (g == 0) {
+        m_out[nb * 4 + t] = m[nb];
+        sum_out[nb * 4 + t] = all;
+      }
+    }
+  }
+  template <int kPass>
+  __device__ __forceinline__ void publish(float* out, int heads) {
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb) {
+      const int h = nb * 4 + t;
+      if (h >= heads) continue;
+#pragma unroll
+      for (int j = 0; j < S::kPassDim / 16; ++j) {
+        const float(&o)[2] = acc[kPass * (S::kPassDim / 16) + j][nb];
+        *reinterpret_cast<float2*>(out + h * S::kJoinRow + j * 16 + 2 * g) = make_float2(o[0], o[1]);
+      }
+    }
   }
 };
 
 // ------------------------------------------------------------------------- kernel -----------
 
+// A segment whose partial results (a slot each: kHeads maxima, kHeads sums, [kHeads][kDim] elements) are
+// complete and left to this CTA to join: those of CTAs c0 .. c0 + n - 1.
+struct Joint {
+  int c0, n, heads;
+  int64_t row;  // of the first head in the output
+};
+
+// Joins them, by the kEndThreads threads that end segments.  The slots are copied to `stage` (room for
+// `stage_bytes`) by bulk copies, all at once or as many as fit, their start spread over the warps
+// (starting one takes 100 to 200 cycles).  For 38 slots, loads to registers take several rounds to L2
+// (4.8 us), and 16-byte cp.async copies 8 us.  `round` counts the uses of the barrier.
+template <typename S>
+__device__ __forceinline__ bool join_partials(const AttnArgs& a, const float* slots, const Joint& j, uint8_t* stage,
+                                              int stage_bytes, int tid, uint64_t* bar, int& round, int* abort) {
+  constexpr int kEach = (S::kHeads * S::kDim / 4 + kEndThreads - 1) / kEndThreads;  // items (4 elements) a thread
+  const int row_items = a.cache.dim / 4, items = j.heads * row_items;
+  const int bytes = (2 * S::kHeads + j.heads * S::kDim) * 4;
+  const int batch = min(j.n, stage_bytes / bytes);
+  float top[kEach], all[kEach], v[kEach][4];
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    top[e] = -INFINITY;
+    all[e] = v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0.0f;
+  }
+  bool ok = true;
+  for (int i0 = 0; i0 < j.n; i0 += batch, ++round) {
+    const int n = min(batch, j.n - i0);
+    if (tid == 0) mbar_arrive_expect_tx(bar, n * bytes);
+    end_sync();  // the stage is free
+    for (int k = tid / 32 + kEndThreads / 32 * (tid % 32); k < n; k += kEndThreads) {
+      const int i = i0 + k;
+      bulk_g2s(stage + k * bytes, slots + (size_t(j.c0 + i) * 2 + (i == 0)) * S::kSlot, bytes, bar);
+    }
+    __syncwarp();
+    ok = wait(bar, round & 1, abort) && ok;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int item = tid + e * kEndThreads;
+      if (item >= items) continue;
+      const int h = item / row_items, d = (item - h * row_items) * 4;
+      const float before = top[e];
+      for (int k = 0; k < n; ++k) top[e] = fmaxf(top[e], *reinterpret_cast<const float*>(stage + k * bytes + h * 4));
+      const float base = top[e] == -INFINITY ? 0.0f : top[e];
+      const float fix = exp2_fast(before - base);
+      all[e] *= fix;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[e][x] *= fix;
+#pragma unroll 2
+      for (int k = 0; k < n; ++k) {
+        const float* p = reinterpret_cast<const float*>(stage + k * bytes);
+        const float f = exp2_fast(p[h] - base);
+        const float4 x = *reinterpret_cast<const float4*>(p + 2 * S::kHeads + h * S::kDim + d);
+        all[e] = fmaf(p[S::kHeads + h], f, all[e]);
+        v[e][0] = fmaf(x.x, f, v[e][0]);
+        v[e][1] = fmaf(x.y, f, v[e][1]);
+        v[e][2] = fmaf(x.z, f, v[e][2]);
+        v[e][3] = fmaf(x.w, f, v[e][3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int item = tid + e * kEndThreads;
+    if (item >= items) continue;
+    const int h = item / row_items, d = (item - h * row_items) * 4;
+    const float scale = all[e] == 0.0f ? 0.0f : 1.0f / all[e];
+    *reinterpret_cast<uint2*>(a.out + (j.row + h) * a.cache.dim + d) =
+        make_uint2(pack_bf16x2(v[e][0] * scale, v[e][1] * scale), pack_bf16x2(v[e][2] * scale, v[e][3] * scale));
+    if (d == 0 && a.lse) a.lse[j.row + h] = all[e] == 0.0f ? -INFINITY : top[e] * kLn2 + logf(all[e]);
+  }
+  return ok;
+}
+
+template <int... I, typename F>
+__device__ __forceinline__ void for_constants(std::integer_sequence<int, I...>, F f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+
 template <typename S>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_decode(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                  int box, int group, int head_blocks) {
+                  int box, int copies, int page_boxes, uint32_t page_magic, int group, int head_blocks) {
   using Control = typename S::Control;
+  using Compute = std::conditional_t<S::kE4M3, WarpE4M3<S>, WarpBf16<S>>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint8_t* exps = smem + S::kExpsAt;
-  float* joined = reinterpret_cast<float*>(smem + S::kOutAt);
+  uint8_t* queries = smem + S::kQueriesAt;
+  float* join = reinterpret_cast<float*>(smem + S::kJoinAt);
   Control* ctl = reinterpret_cast<Control*>(smem + S::kControlAt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const CacheDev& c = a.cache;
@@ -221,44 +793,65 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&ctl->full[i], 1);
+      // each producer warp, and in the E4M3 form the lanes of the one that copies the exponents
+      mbar_init(&ctl->full[i], kProducers + (S::kE4M3 ? 32 : 0));
       mbar_init(&ctl->empty[i], S::kGroupWarps);
     }
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&ctl->q_full[i], 1);
+      mbar_init(&ctl->q_empty[i], kWarps);
+    }
+    mbar_init(&ctl->join_full, kWarps);
+    mbar_init(&ctl->join_empty, kEndThreads / 32);
+    mbar_init(&ctl->merge_full, 1);
     ctl->abort = 0;
     mbar_fence_init();
+    prefetch_map(&map_k);
+    prefetch_map(&map_v);
   }
+  // What a producer warp needs that no earlier kernel writes: lane's copy of every tile (one of keys or
+  // values, one span or all, one box).
+  const int me = warp - kWarps;
+  const int boxes = S::kTokens / box;    // of a tile: 1, 2, 4 or 8
+  const int box_shift = __ffs(2 * copies) - 1, row_shift = __ffs(box) - 1;
+  const uint32_t job_bytes = uint32_t(box * S::kRow) >> (box_shift - 1);
+  const int job = lane * kProducers + me;  // values after keys, span by span, box by box
+  const bool has_job = job < boxes << box_shift;
+  const int job_box = has_job ? job >> box_shift : 0, job_span = (job & (2 * copies - 1)) >> 1;
+  const CUtensorMap* job_map = job & 1 ? &map_v : &map_k;
+  const uint32_t job_at = smem_u32(smem) + (job & 1) * S::kTile + job_box * box * S::kRow + job_span * box * S::kSpan;
   pdl_begin();
 
   // The line's length and the place where this CTA's part begins.
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b_lo = min(a.B, int(threadIdx.x) * per), b_hi = min(a.B, b_lo + per);
-  long long mine = 0;
+  int mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
-    mine += (long long)span_of<S>(a, b).tiles * segs;
+    mine += span_of<S>(a, b).tiles * segs;
     if (blockIdx.x == 0 && __ldg(a.lens + b) > a.table.max_pages * c.page) report_bad_page(a.table.status_flags);
   }
-  long long upto = mine;
+  int upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
   if (lane == 31) ctl->scan[warp] = upto;
   __syncthreads();
-  long long total = 0;
+  int total = 0;
 #pragma unroll
-  for (int w = 0; w <= kWarps; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w == warp) upto += total;
     total += ctl->scan[w];
   }
-  const long long ctas = min((long long)gridDim.x, total);
+  const int ctas = min(int(gridDim.x), total);
+  const Parts line(total, ctas);
   const bool working = blockIdx.x < ctas;
-  const long long lo = working ? total * blockIdx.x / ctas : 0, hi = working ? total * (blockIdx.x + 1) / ctas : 0;
+  const int lo = working ? line.begin(blockIdx.x) : 0, hi = working ? line.begin(blockIdx.x + 1) : 0;
   if (lo < hi && lo >= upto - mine && lo < upto) {
-    long long at = upto - mine;
-    int b = b_lo;
+    int at = upto - mine, b = b_lo;
     for (;; ++b) {
-      const long long n = (long long)span_of<S>(a, b).tiles * segs;
+      const int n = span_of<S>(a, b).tiles * segs;
       if (lo < at + n) break;
       at += n;
     }
@@ -267,511 +860,269 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
+  // Every warp walks the CTA's part by itself; `it` counts its tiles (the ring's position), `seg` its
+  // segments.  Only the producers' and the query warp's walks end early, at a wait that ran out: the
+  // others go on through the same barriers on whatever they find, and the status record says that it
+  // is no result.
   Walk<S> walk;
-  walk.start(a, segs, ctl->b0, ctl->off0, lo, hi);
-  int it = 0;  // tiles of this CTA so far: the ring's position
+  walk.start(a, ctl->b0, ctl->off0, lo, hi);
+  int it = 0, seg = 0;
 
-  if (warp == kWarps) {
-    // ---------------------------------------------------------------- producer --------------
-    const int boxes = S::kTokens / box;
-    const uint32_t box_bits = (1u << (box / 16)) - 1u;
-    const uint32_t box_bytes = uint32_t(box) * (2 * S::kRow + (S::kE4M3 ? 2 : 0));
-    bool ok = true;
-    for (; ok && !walk.done(); walk.next(a, segs)) {
-      const int kv = walk.seg / head_blocks;
-      const int32_t* pages = a.table.pages + int64_t(walk.b) * a.table.max_pages;
-      const int t_end = walk.span.tile0 + walk.tile + walk.take;
-      // a box's page: looked up a tile ahead of its copies
-      auto look_up = [&](int tile) {
-        const int p = tile * S::kTokens + lane * box;
-        return lane < boxes && tile < t_end && p < walk.span.end && p + box > walk.span.first ? __ldg(pages + p / c.page)
-                                                                                             : -1;
-      };
-      int page = look_up(walk.span.tile0 + walk.tile);
-      for (int tile = walk.span.tile0 + walk.tile; tile < t_end; ++tile, ++it) {
-        const int page_next = look_up(tile + 1);
-        const int p0 = tile * S::kTokens + lane * box;
-        const bool wanted = lane < boxes && p0 < walk.span.end && p0 + box > walk.span.first;
-        const bool good = wanted && page >= 0 && page < c.n_pages;
-        if (wanted && !good) report_bad_page(a.table.status_flags);
-        const uint32_t copied = __ballot_sync(0xffffffffu, good);
-        const int stage = it % S::kStages;
-        ok = mbar_wait(&ctl->empty[stage], ((it / S::kStages) & 1) ^ 1, &ctl->abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) {
-          uint32_t bits = 0;
-          for (int i = 0; i < boxes; ++i)
-            if (copied >> i & 1) bits |= box_bits << (i * (box / 16));
-          ctl->valid[stage] = bits;
-          mbar_arrive_expect_tx(&ctl->full[stage], __popc(copied) * box_bytes);
-        }
-        __syncwarp();
-        const uint32_t bar = smem_u32(&ctl->full[stage]);
-        const uint32_t dst = smem_u32(smem + size_t(stage) * S::kStage);
-        const int jobs = 2 * boxes * S::kSpans;  // keys first
-        for (int j0 = 0; j0 < jobs; j0 += 32) {
-          const int j = j0 + lane;
-          const int i = j % boxes, span = j / boxes % S::kSpans, is_v = j / (boxes * S::kSpans);
-          const int pg = __shfl_sync(0xffffffffu, page, i);
-          if (j < jobs && (copied >> i & 1)) {
-            const int p = tile * S::kTokens + i * box;
-            tma_load_4d(dst + is_v * S::kTile + span * (S::kTokens * S::kSpan) + i * box * S::kSpan,
-                        is_v ? &map_v : &map_k, span * S::kSpanElems, p % c.page, kv, pg, bar);
+  if (warp >= kWarps && warp < kEndWarp) {
+    fewer_registers<kProducerRegs>();
+    if (warp < kQueryWarp) {
+      // --------------------------------------------------------------- producers ------------
+      bool ok = true;
+      for (; ok && !walk.done(); walk.next(a, segs)) {
+        const int kv = walk.seg / head_blocks;
+        const int t_begin = walk.span.tile0 + walk.tile;
+        const int32_t* pages = a.table.pages + int64_t(walk.b) * a.table.max_pages;
+        // The pages of 32 boxes at a time, a lane each, and of the next 32 ahead of their use; with the
+        // row in the page (the division by the page size is not for every tile).
+        struct Boxes {
+          int page, row;
+        };
+        auto look_up = [&](int rel) {
+          const int i = t_begin * boxes + rel + lane, p = i << row_shift;
+          const int slot = page_boxes == 1 ? i : __umulhi(i, page_magic);  // i / page_boxes
+          const bool wanted = rel + lane < walk.take * boxes && p < walk.span.end && p + box > walk.span.first;
+          return Boxes{wanted ? __ldg(pages + slot) : -1, (i - slot * page_boxes) << row_shift};
+        };
+        Boxes cur = look_up(0), ahead = look_up(32);
+        for (int n = 0; n < walk.take; ++n, ++it) {
+          const int off = (n * boxes) & 31;
+          if (n > 0 && off == 0) {
+            cur = ahead;
+            ahead = look_up(n * boxes + 32);
+          }
+          // lane i < boxes: box i of the tile, its page and the row of the cache where it begins
+          const int p0 = (t_begin + n) * S::kTokens + lane * box;
+          const bool wanted = lane < boxes && p0 < walk.span.end && p0 + box > walk.span.first;
+          const int page = __shfl_sync(0xffffffffu, cur.page, (off + lane) & 31);
+          const int in_page = __shfl_sync(0xffffffffu, cur.row, (off + lane) & 31);
+          const bool good = wanted && page >= 0 && page < c.n_pages;
+          if (wanted && !good) report_bad_page(a.table.status_flags);
+          const int row = good ? (page * c.heads + kv) * c.page + in_page : 0;  // below 2^31
+          const uint32_t copied = __ballot_sync(0xffffffffu, good);
+          const int job_row = __shfl_sync(0xffffffffu, row, job_box);
+          const bool mine_too = has_job && (copied >> job_box & 1);
+          const uint32_t bits = __ballot_sync(0xffffffffu, lane < S::kTokens / 16 && (copied >> (lane * 16 >> row_shift) & 1));
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine_too)) * job_bytes;
+          const int stage = it % S::kStages;
+          ok = __all_sync(0xffffffffu, wait(&ctl->empty[stage], ((it / S::kStages) & 1) ^ 1, &ctl->abort));
+          if (!ok) break;
+          uint64_t* bar = &ctl->full[stage];
+          if (lane == 0) {
+            if (me == 0) ctl->valid[stage] = bits;
+            mbar_arrive_expect_tx(bar, bytes);
+          }
+          __syncwarp();
+          if (mine_too) tma_load_rows(job_at + stage * S::kStage, job_map, job_span * S::kSpanElems, job_row, bar);
+          if constexpr (S::kE4M3) {
+            if (me == kProducers - 1) {
+              // the exponents of 16 tokens a lane (16 bytes: too little for a bulk copy to pay)
+              constexpr int kPieces = S::kTokens / 16;
+              const int r = lane % kPieces * 16, i = r >> row_shift, is_v = lane / kPieces;
+              const int y = __shfl_sync(0xffffffffu, row, i) + (r & (box - 1));
+              if (is_v < 2 && (copied >> i & 1))
+                cp_async16(exps + stage * S::kExps + is_v * S::kTokens + r, (is_v ? c.v_exp : c.k_exp) + y);
+              cp_async_arrive_noinc(bar);
+            }
           }
         }
-        if constexpr (S::kE4M3) {
-          const int i = lane % boxes, is_v = lane / boxes;  // boxes <= 8
-          const int pg = __shfl_sync(0xffffffffu, page, i);
-          if (is_v < 2 && (copied >> i & 1)) {
-            const int p = tile * S::kTokens + i * box;
-            const uint8_t* src = (is_v ? c.v_exp : c.k_exp) + (int64_t(pg) * c.heads + kv) * c.page + p % c.page;
-            bulk_g2s(exps + stage * S::kExps + is_v * S::kTokens + i * box, src, box, &ctl->full[stage]);
-          }
-        }
-        page = page_next;
       }
-    }
-    if (!ok && lane == 0) {
-      // some wait ran out: this CTA's copies must land before it ends (bounded again)
-      report_timeout_flag(a.table.status_flags, 40);
-      const unsigned long long t0 = global_timer_ns();
-      for (int i = max(0, it - S::kStages); i < it; ++i)
-        while (!mbar_try_wait(&ctl->full[i % S::kStages], (i / S::kStages) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
+      if (!ok && lane == 0) {
+        // a wait ran out: this CTA's copies must land before it ends (bounded again)
+        report_timeout_flag(a.table.status_flags, 40);
+        const unsigned long long t0 = global_timer_ns();
+        for (int i = max(0, it - S::kStages); i < it; ++i)
+          while (!mbar_try_wait(&ctl->full[i % S::kStages], (i / S::kStages) & 1) &&
+                 global_timer_ns() - t0 < kWaitLimitNs) {
+          }
+      }
+    } else if (warp == kQueryWarp) {
+      // ---------------------------------------------------------------- queries -------------
+      for (; !walk.done(); walk.next(a, segs), ++seg) {
+        const int kv = walk.seg / head_blocks, hb = walk.seg % head_blocks, slot = seg % S::kSlots;
+        if (!__all_sync(0xffffffffu, wait(&ctl->q_empty[slot], ((seg / S::kSlots) & 1) ^ 1, &ctl->abort))) {
+          if (lane == 0) report_timeout_flag(a.table.status_flags, 41);
+          break;
         }
+        Compute::lay_out(queries + slot * S::kQueries,
+                         a.q + walk.b * a.q_stride + int64_t(kv * group + hb * S::kHeads) * c.dim,
+                         min(S::kHeads, group - hb * S::kHeads), c.dim, a.scale * kLog2e, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->q_full[slot]);
+      }
+    } else {
+      // ------------------------------------------- sequences without a token: zeros ---------
+      for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (span_of<S>(a, b).tiles != 0) continue;
+        const int n = a.n_heads * c.dim / 8;
+        uint4* out = reinterpret_cast<uint4*>(a.out + int64_t(b) * a.n_heads * c.dim);
+        if (warp == kQueryWarp + 1) {
+          for (int i = lane; i < n; i += 32) out[i] = make_uint4(0, 0, 0, 0);
+          if (a.lse)
+            for (int h = lane; h < a.n_heads; h += 32) a.lse[int64_t(b) * a.n_heads + h] = -INFINITY;
+        }
+      }
     }
     return;
   }
 
-  // ------------------------------------------------------------------ consumers -------------
-  const int g = lane >> 2, t = lane & 3;
-  const int wg = warp / S::kGroupWarps, row0 = (warp % S::kGroupWarps) * S::kPerWarp;
-  constexpr int kMT = S::kPerWarp / 16;     // blocks of 16 tokens
-  constexpr int kKS = S::kDim / 16;         // steps of 16 elements
-  constexpr int kNB = S::kBlocks;
-  bool timed_out = false;
-
-  // sequences without a token: zeros
-  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    if (span_of<S>(a, b).tiles != 0) continue;
-    const int n = a.n_heads * c.dim / 8;
-    uint4* out = reinterpret_cast<uint4*>(a.out + int64_t(b) * a.n_heads * c.dim);
-    for (int i = threadIdx.x; i < n; i += kWarps * 32) out[i] = make_uint4(0, 0, 0, 0);
-    if (a.lse)
-      for (int h = threadIdx.x; h < a.n_heads; h += kWarps * 32) a.lse[int64_t(b) * a.n_heads + h] = -INFINITY;
+  if (warp < kWarps) {
+    // ------------------------------------------------------------------ compute -------------
+    more_registers<kComputeRegs>();
+    const int wg = warp / S::kGroupWarps, row0 = (warp % S::kGroupWarps) * S::kPerWarp;
+    bool timed_out = false;
+    int joins = 0;  // passes through the join buffer so far
+    Compute mine_w(row0, lane, box);
+    for (; !walk.done(); walk.next(a, segs), ++seg) {
+      const int hb = walk.seg % head_blocks, slot = seg % S::kSlots;
+      if (!wait(&ctl->q_full[slot], (seg / S::kSlots) & 1, &ctl->abort)) timed_out = true;
+      mine_w.begin(queries + slot * S::kQueries, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_empty[slot]);
+      TileView tv;
+      tv.first = walk.span.first;
+      tv.end = walk.span.end;
+      for (int n = 0; n < walk.take; ++n, ++it) {
+        const int stage = it % S::kStages;
+        if (stage % S::kGroups != wg) continue;
+        if (!wait(&ctl->full[stage], (it / S::kStages) & 1, &ctl->abort)) timed_out = true;
+        tv.k = smem_u32(smem + size_t(stage) * S::kStage);
+        tv.v = tv.k + S::kTile;
+        tv.exps = exps + stage * S::kExps + row0;
+        tv.pos0 = (walk.span.tile0 + walk.tile + n) * S::kTokens + row0;
+        constexpr uint32_t kAll = (1u << (S::kPerWarp / 16)) - 1u;
+        tv.valid = ctl->valid[stage] >> (row0 / 16) & kAll;
+        if (tv.valid == kAll && tv.pos0 >= tv.first && tv.pos0 + S::kPerWarp <= tv.end)
+          mine_w.template tile<true>(tv);
+        else if (tv.valid != 0)
+          mine_w.template tile<false>(tv);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->empty[stage]);
+      }
+      const int heads = min(S::kHeads, group - hb * S::kHeads);
+      for_constants(std::make_integer_sequence<int, S::kPasses>{}, [&](auto pass) {
+        constexpr int kPass = decltype(pass)::value;
+        if (kPass * S::kPassDim >= c.dim) return;
+        if (!wait(&ctl->join_empty, (joins & 1) ^ 1, &ctl->abort)) timed_out = true;
+        if (kPass == 0) mine_w.publish_sums(ctl->m[warp], ctl->sum[warp]);
+        mine_w.template publish<kPass>(join + warp * S::kJoinWarp, heads);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->join_full);
+        ++joins;
+      });
+    }
+    if (timed_out && lane == 0) report_timeout_flag(a.table.status_flags, 42);
+    return;
   }
 
-  // ldmatrix addresses.  A 16-byte chunk i of row r of a tile lies at chunk i ^ (r % 8) of the row
-  // (128-byte rows), or i ^ (r / 2 % 4) (64-byte rows).  `lo_row`: lanes 8-15 and 24-31 address rows
-  // 8 further, lanes 16-31 the next chunk; `lo_chunk` the other way round.
-  constexpr bool kNarrow = S::kSpan == 64;
-  const int r8 = lane & 7;
-  auto swizzle = [&](int row) { return kNarrow ? (row >> 1) & 3 : row & 7; };
-  const int a_row = row0 + r8 + ((lane >> 3) & 1) * 8, a_hi = lane >> 4;
-  const int v_row = S::kE4M3 ? a_row : row0 + r8 + (lane >> 4) * 8, v_hi = S::kE4M3 ? a_hi : (lane >> 3) & 1;
-  const uint32_t k_off = uint32_t(a_row * S::kSpan), k_x = uint32_t((a_hi ^ swizzle(a_row)) << 4);
-  const uint32_t v_off = uint32_t(v_row * S::kSpan), v_x = uint32_t((v_hi ^ swizzle(v_row)) << 4);
-  // byte offset of chunks 2 i (and 2 i + 1, by lane) in a tile; rows 16 further do not change the swizzle
-  constexpr int kPairs = S::kSpan / 32;
-  auto chunk = [&](int i, uint32_t x) {
-    return uint32_t(i / kPairs * (S::kTokens * S::kSpan)) + (uint32_t((i % kPairs) << 5) ^ x);
-  };
-
+  // ---------------------------------------------------------------------- segment ends ------
+  fewer_registers<kEndRegs>();
+  const int tid = threadIdx.x - kEndWarp * 32;
+  bool timed_out = false;
+  int joins = 0, n_joints = 0;
+  Joint joints[2] = {};
   for (; !walk.done(); walk.next(a, segs)) {
     const int kv = walk.seg / head_blocks, hb = walk.seg % head_blocks;
-    const int head0 = kv * group + hb * S::kHeads;             // first query head
-    const int heads = min(S::kHeads, group - hb * S::kHeads);  // of this segment
+    const int heads = min(S::kHeads, group - hb * S::kHeads);
+    const int64_t row = int64_t(walk.b) * a.n_heads + kv * group + hb * S::kHeads;  // of the first head in out
+    const bool whole = walk.take == walk.span.tiles;  // finished here, or a partial result
+    float* slots = reinterpret_cast<float*>(a.ws + kAttnPartialsAt);
+    // slot 0: a segment that began before this CTA's part; slot 1: one that begins in it
+    float* slot = slots + (size_t(blockIdx.x) * 2 + (walk.tile == 0)) * S::kSlot;
 
-    // the queries as B fragments: lane (g, t) has head g's elements 2t, 2t+1, 2t+8, 2t+9 of each
-    // step (bf16), or 4t .. 4t+3 (E4M3: the order in which ldmatrix delivers the codes)
-    uint32_t qf[kKS][kNB][2];
-    float factor[kNB][2];  // scores to base-2 exponents, for heads 2t and 2t+1
-#pragma unroll
-    for (int nb = 0; nb < kNB; ++nb) {
-      const bool live = nb * 8 + g < heads;
-      const __nv_bfloat16* q = a.q + walk.b * a.q_stride + int64_t(head0 + (live ? nb * 8 + g : 0)) * c.dim;
-#pragma unroll
-      for (int ks = 0; ks < kKS; ++ks) {
-        const bool in = live && ks * 16 < c.dim;  // head_dim is a multiple of 16
-        if constexpr (S::kE4M3) {
-          const uint2 u = in ? *reinterpret_cast<const uint2*>(q + ks * 16 + 4 * t) : make_uint2(0, 0);
-          qf[ks][nb][0] = u.x;
-          qf[ks][nb][1] = u.y;
-        } else {
-          qf[ks][nb][0] = in ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 2 * t) : 0;
-          qf[ks][nb][1] = in ? *reinterpret_cast<const uint32_t*>(q + ks * 16 + 2 * t + 8) : 0;
-        }
-      }
-      factor[nb][0] = factor[nb][1] = a.scale * kLog2e;
-      if constexpr (S::kE4M3) {
-        // head g's queries times 2^-e, the largest between 2^14 and 2^15, as fp16
-        float top = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[ks][nb][i] << 16)),
-                                   fabsf(__uint_as_float(qf[ks][nb][i] & 0xffff0000u))));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = min(113, max(-100, int(__float_as_uint(top) >> 23) - 127 - 14));
-        const float down = __uint_as_float(uint32_t(127 - e) << 23);
-#pragma unroll
-        for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            qf[ks][nb][i] = pack_half2(__uint_as_float(qf[ks][nb][i] << 16) * down,
-                                       __uint_as_float(qf[ks][nb][i] & 0xffff0000u) * down);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          factor[nb][i] *= __uint_as_float(uint32_t(127 + __shfl_sync(0xffffffffu, e, 8 * t + 4 * i)) << 23);
-      }
-    }
-
-    float m[kNB][2], sum[kNB][2], acc[kKS][kNB][4];
-#pragma unroll
-    for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) m[nb][i] = -INFINITY, sum[nb][i] = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-      for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[ks][nb][i] = 0.0f;
-
-    const int t_begin = walk.span.tile0 + walk.tile;
-    for (int n = 0; n < walk.take; ++n, ++it) {
-      if (it % S::kGroups != wg) continue;
-      const int stage = it % S::kStages;
-      if (!mbar_wait(&ctl->full[stage], (it / S::kStages) & 1, &ctl->abort)) timed_out = true;
-      const uint32_t k_tile = smem_u32(smem + size_t(stage) * S::kStage), v_tile = k_tile + S::kTile;
-      const int pos0 = (t_begin + n) * S::kTokens + row0;  // of this warp's first token
-      const uint32_t valid = ctl->valid[stage] >> (row0 / 16);
-      constexpr uint32_t kAll = (1u << kMT) - 1u;
-      const bool whole = (valid & kAll) == kAll && pos0 >= walk.span.first && pos0 + S::kPerWarp <= walk.span.end;
-
-      if ((valid & kAll) != 0) {
-        // scores: tokens g and g + 8 of each block, heads 2t and 2t + 1
-        float s[kMT][kNB][4];
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          float s2[kNB][4];  // two chains of products
-#pragma unroll
-          for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][nb][i] = s2[nb][i] = 0.0f;
-          const uint32_t rows = k_tile + k_off + mt * 16 * S::kSpan;
-          if constexpr (S::kE4M3) {
-#pragma unroll
-            for (int ks = 0; ks < kKS; ks += 2) {
-              uint32_t r[4];
-              ldmatrix4(rows + chunk(ks / 2, k_x), r);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t a0 = half2_of_codes(r[2 * h] & 0xffffu), a1 = half2_of_codes(r[2 * h + 1] & 0xffffu);
-                const uint32_t a2 = half2_of_codes(r[2 * h] >> 16), a3 = half2_of_codes(r[2 * h + 1] >> 16);
-#pragma unroll
-                for (int nb = 0; nb < kNB; ++nb)
-                  mma<true>(h ? s2[nb] : s[mt][nb], a0, a1, a2, a3, qf[ks + h][nb][0], qf[ks + h][nb][1]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int ks = 0; ks < kKS; ++ks) {
-              uint32_t r[4];
-              ldmatrix4(rows + chunk(ks, k_x), r);
-#pragma unroll
-              for (int nb = 0; nb < kNB; ++nb)
-                mma<false>(ks & 1 ? s2[nb] : s[mt][nb], r[0], r[1], r[2], r[3], qf[ks][nb][0], qf[ks][nb][1]);
-            }
-          }
-#pragma unroll
-          for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[mt][nb][i] += s2[nb][i];
-        }
-
-        // exponents: t of each (token, head), and the values' exponents
-        float c_exp[kMT][2], c_unit[kMT][2];  // of tokens g and g + 8: in m, and as a factor
-        float top[kNB][2];
-#pragma unroll
-        for (int nb = 0; nb < kNB; ++nb) top[nb][0] = top[nb][1] = -INFINITY;
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int r = mt * 16 + half * 8 + g;
-            const bool seen = whole || ((valid >> mt & 1) && pos0 + r >= walk.span.first && pos0 + r < walk.span.end);
-            float unit = 1.0f;
-            c_exp[mt][half] = 0.0f;
-            c_unit[mt][half] = 1.0f;
-            if constexpr (S::kE4M3) {
-              const uint8_t* e = exps + stage * S::kExps + row0 + r;
-              unit = exp_value(e[0]);
-              const uint32_t ve = e[S::kTokens];
-              c_exp[mt][half] = float(max(int(ve) - kExpBias, kMinExp));
-              c_unit[mt][half] = seen ? exp_value(ve) : 0.0f;
-            }
-#pragma unroll
-            for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float& x = s[mt][nb][2 * half + i];
-                x = seen ? x * (factor[nb][i] * unit) : -INFINITY;
-                top[nb][i] = fmaxf(top[nb][i], x + c_exp[mt][half]);
-              }
-          }
-        float base[kNB][2], fix[kNB][2];
-        bool moved = false;
-#pragma unroll
-        for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float now = fmaxf(m[nb][i], max_over_rows(top[nb][i]));
-            base[nb][i] = now == -INFINITY ? 0.0f : now;  // nothing seen yet: exp2(-inf - 0) = 0
-            fix[nb][i] = exp2_fast(m[nb][i] - base[nb][i]);
-            moved |= now != m[nb][i];
-            m[nb][i] = now;
-          }
-        if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-          for (int nb = 0; nb < kNB; ++nb) {
-            sum[nb][0] *= fix[nb][0];
-            sum[nb][1] *= fix[nb][1];
-#pragma unroll
-            for (int ks = 0; ks < kKS; ++ks) {
-              acc[ks][nb][0] *= fix[nb][0];
-              acc[ks][nb][1] *= fix[nb][1];
-              acc[ks][nb][2] *= fix[nb][0];
-              acc[ks][nb][3] *= fix[nb][1];
-            }
-          }
-        }
-        // weights, as the B operand of the product with the values
-        uint32_t w[kMT][kNB][2];
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-          for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float p0 = exp2_fast(s[mt][nb][2 * half] - base[nb][0]);
-              const float p1 = exp2_fast(s[mt][nb][2 * half + 1] - base[nb][1]);
-              sum[nb][0] += p0;
-              sum[nb][1] += p1;
-              w[mt][nb][half] = transpose8x8(S::kE4M3 ? pack_half2(p0 * c_unit[mt][half], p1 * c_unit[mt][half])
-                                                      : pack_bf16x2(p0, p1));
-            }
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          if (!(valid >> mt & 1)) continue;  // nothing was copied there (all weights are 0)
-          // what lies in rows that are not seen is no number: 0 there (tokens 2t, 2t+1, 2t+8, 2t+9)
-          uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-          if (!whole)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int p = pos0 + mt * 16 + half * 8 + 2 * t;
-              keep[half] = (p >= walk.span.first && p < walk.span.end ? 0xffffu : 0u) |
-                           (p + 1 >= walk.span.first && p + 1 < walk.span.end ? 0xffff0000u : 0u);
-            }
-          const uint32_t rows = v_tile + v_off + mt * 16 * S::kSpan;
-          if constexpr (S::kE4M3) {
-#pragma unroll
-            for (int ks = 0; ks < kKS; ks += 2) {
-              uint32_t r[4];
-              ldmatrix4_trans(rows + chunk(ks / 2, v_x), r);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                // codes of elements 2g (bytes 0 and 2: two tokens) and 2g + 1 (bytes 1 and 3)
-                const uint32_t lo = r[2 * h] & (whole ? 0xffffffffu : keep[0]);
-                const uint32_t hi = r[2 * h + 1] & (whole ? 0xffffffffu : keep[1]);
-                const uint32_t a0 = half2_of_codes(__byte_perm(lo, 0, 0x4420)),
-                               a1 = half2_of_codes(__byte_perm(lo, 0, 0x4431)),
-                               a2 = half2_of_codes(__byte_perm(hi, 0, 0x4420)),
-                               a3 = half2_of_codes(__byte_perm(hi, 0, 0x4431));
-#pragma unroll
-                for (int nb = 0; nb < kNB; ++nb) mma<true>(acc[ks + h][nb], a0, a1, a2, a3, w[mt][nb][0], w[mt][nb][1]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int ks = 0; ks < kKS; ++ks) {
-              uint32_t r[4];
-              ldmatrix4_trans(rows + chunk(ks, v_x), r);
-              if (!whole) r[0] &= keep[0], r[1] &= keep[0], r[2] &= keep[1], r[3] &= keep[1];
-#pragma unroll
-              for (int nb = 0; nb < kNB; ++nb)
-                mma<false>(acc[ks][nb], r[0], r[1], r[2], r[3], w[mt][nb][0], w[mt][nb][1]);
-            }
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->empty[stage]);
-    }
-
-    // -------- the warps' results of this segment joined in shared memory --------
-#pragma unroll
-    for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float s = sum_over_rows(sum[nb][i]);
-        if (g == 0) {
-          ctl->m[warp][nb * 8 + 2 * t + i] = m[nb][i];
-          ctl->sum[warp][nb * 8 + 2 * t + i] = s;
-        }
-      }
-    consumers_sync();
-    float fix[kNB][2];
-#pragma unroll
-    for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = nb * 8 + 2 * t + i;
+    // -------- the warps' results --------
+    for (int d0 = 0; d0 < c.dim; d0 += S::kPassDim, ++joins) {
+      if (!wait(&ctl->join_full, joins & 1, &ctl->abort)) timed_out = true;
+      constexpr int kVecs = S::kPassDim / 4;
+      for (int i = tid; i < heads * kVecs; i += kEndThreads) {
+        const int h = i / kVecs, d = (i % kVecs) * 4;
         float top = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ctl->m[w][h]);
         const float base = top == -INFINITY ? 0.0f : top;
-        fix[nb][i] = exp2_fast(m[nb][i] - base);
-        if (warp == 0 && g == 0) {
-          float all = 0.0f;
+        float all = 0.0f, v[4] = {};
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) all += ctl->sum[w][h] * exp2_fast(ctl->m[w][h] - base);
-          ctl->total_m[h] = top;
-          ctl->total_sum[h] = all;
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = exp2_fast(ctl->m[w][h] - base);
+          const float4 x = *reinterpret_cast<const float4*>(join + w * S::kJoinWarp + h * S::kJoinRow + d);
+          all = fmaf(ctl->sum[w][h], f, all);
+          v[0] = fmaf(x.x, f, v[0]);
+          v[1] = fmaf(x.y, f, v[1]);
+          v[2] = fmaf(x.z, f, v[2]);
+          v[3] = fmaf(x.w, f, v[3]);
         }
-      }
-    // A part of the width a warp and round, another one each round: every element is added up over
-    // the warps in a fixed order, and all warps are busy.
-    constexpr int kParts = kKS < kWarps ? kKS : kWarps, kPartSteps = kKS / kParts;
-#pragma unroll 1
-    for (int round = 0; round < kWarps; ++round) {
-      const int part = (warp + round) % kWarps;
-#pragma unroll
-      for (int ks = 0; ks < kKS; ++ks) {
-        if (part != ks / kPartSteps) continue;
-#pragma unroll
-        for (int nb = 0; nb < kNB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float* at = joined + (nb * 8 + 2 * t + i) * S::kOutLd + ks * 16;
-            const float x0 = acc[ks][nb][i] * fix[nb][i], x1 = acc[ks][nb][2 + i] * fix[nb][i];
-            float* p0 = at + (S::kE4M3 ? 2 * g : g);
-            float* p1 = at + (S::kE4M3 ? 2 * g + 1 : g + 8);
-            if (round == 0) {
-              *p0 = x0;
-              *p1 = x1;
-            } else {
-              *p0 += x0;
-              *p1 += x1;
-            }
-          }
-      }
-      consumers_sync();
-    }
-
-    // -------- finished here, or a partial result --------
-    const int vecs = c.dim / 8;
-    const long long seg_at = walk.pos - walk.tile;  // the segment's place on the line
-    if (walk.take == walk.span.tiles) {
-      for (int i = threadIdx.x; i < heads * vecs; i += kWarps * 32) {
-        const int h = i / vecs, d = (i - h * vecs) * 8;
-        const float all = ctl->total_sum[h], scale = all == 0.0f ? 0.0f : 1.0f / all;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = joined[h * S::kOutLd + d + j] * scale;
-        store_vec8(a.out + (int64_t(walk.b) * a.n_heads + head0 + h) * c.dim + d, v);
-      }
-      if (a.lse && threadIdx.x < heads) {
-        const float all = ctl->total_sum[threadIdx.x];
-        a.lse[int64_t(walk.b) * a.n_heads + head0 + threadIdx.x] =
-            all == 0.0f ? -INFINITY : ctl->total_m[threadIdx.x] * kLn2 + logf(all);
-      }
-    } else {
-      // slot 0: a segment that began before this CTA's part; slot 1: one that begins in it
-      float* slots = reinterpret_cast<float*>(a.ws + kAttnPartialsAt);
-      float* slot = slots + (size_t(blockIdx.x) * 2 + (walk.tile == 0)) * S::kSlot;
-      for (int i = threadIdx.x; i < heads * c.dim / 4; i += kWarps * 32) {
-        const int h = i / (c.dim / 4), d = (i - h * (c.dim / 4)) * 4;
-        __stcg(reinterpret_cast<float4*>(slot + 2 * S::kHeads + h * S::kDim + d),
-               *reinterpret_cast<const float4*>(joined + h * S::kOutLd + d));
-      }
-      if (threadIdx.x < heads) {
-        __stcg(slot + threadIdx.x, ctl->total_m[threadIdx.x]);
-        __stcg(slot + S::kHeads + threadIdx.x, ctl->total_sum[threadIdx.x]);
-      }
-      __threadfence();
-      consumers_sync();
-      // the CTAs whose parts hold the segment's first and last tile
-      const int c0 = int(((seg_at + 1) * ctas - 1) / total);
-      const int c1 = int(((seg_at + walk.span.tiles) * ctas - 1) / total);
-      int* counter = reinterpret_cast<int*>(a.ws + kAttnTicketsAt) + c0;
-      if (threadIdx.x == 0) {
-        const int before = atomicAdd(counter, 1);
-        ctl->last = before == c1 - c0;
-        if (before == c1 - c0) *counter = 0;
-      }
-      consumers_sync();
-      if (ctl->last) {
-        __threadfence();
-        const int n = c1 - c0 + 1;
-        auto slot_of = [&](int i) { return slots + (size_t(c0 + i) * 2 + (i == 0)) * S::kSlot; };
-        for (int h = warp; h < heads; h += kWarps) {
-          float top = -INFINITY, all = 0.0f;
-          for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(slot_of(i) + h));
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float base = top == -INFINITY ? 0.0f : top;
-          for (int i = lane; i < n; i += 32)
-            all += __ldcg(slot_of(i) + S::kHeads + h) * exp2_fast(__ldcg(slot_of(i) + h) - base);
-          all = warp_sum(all);
-          if (lane == 0) {
-            ctl->total_m[h] = base;
-            ctl->total_sum[h] = all;
-            if (a.lse)
-              a.lse[int64_t(walk.b) * a.n_heads + head0 + h] = all == 0.0f ? -INFINITY : base * kLn2 + logf(all);
-          }
-        }
-        consumers_sync();
-        for (int i = threadIdx.x; i < heads * c.dim / 4; i += kWarps * 32) {
-          const int h = i / (c.dim / 4), d = (i - h * (c.dim / 4)) * 4;
-          const float base = ctl->total_m[h], all = ctl->total_sum[h];
-          float v[4] = {};
-#pragma unroll 8
-          for (int k = 0; k < n; ++k) {
-            const float* p = slot_of(k);
-            const float f = exp2_fast(__ldcg(p + h) - base);
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(p + 2 * S::kHeads + h * S::kDim + d));
-            v[0] = fmaf(x.x, f, v[0]);
-            v[1] = fmaf(x.y, f, v[1]);
-            v[2] = fmaf(x.z, f, v[2]);
-            v[3] = fmaf(x.w, f, v[3]);
-          }
+        if (whole) {
           const float scale = all == 0.0f ? 0.0f : 1.0f / all;
-          *reinterpret_cast<uint2*>(a.out + (int64_t(walk.b) * a.n_heads + head0 + h) * c.dim + d) =
-              make_uint2(pack_bf16x2(v[0] * scale, v[1] * scale), pack_bf16x2(v[2] * scale, v[3] * scale));
+          if (d0 + d < c.dim)
+            *reinterpret_cast<uint2*>(a.out + (row + h) * c.dim + d0 + d) =
+                make_uint2(pack_bf16x2(v[0] * scale, v[1] * scale), pack_bf16x2(v[2] * scale, v[3] * scale));
+          if (d0 == 0 && d == 0 && a.lse) a.lse[row + h] = all == 0.0f ? -INFINITY : base * kLn2 + logf(all);
+        } else {
+          if (d0 + d < c.dim)
+            __stcg(reinterpret_cast<float4*>(slot + 2 * S::kHeads + h * S::kDim + d0 + d),
+                   make_float4(v[0], v[1], v[2], v[3]));
+          if (d0 == 0 && d == 0) {
+            __stcg(slot + h, top);
+            __stcg(slot + S::kHeads + h, all);
+          }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->join_empty);
     }
-    consumers_sync();  // the join buffer is free again
+    if (whole) continue;
+
+    // -------- the last of the segment's CTAs joins the partial results, at its own end --------
+    // the CTAs whose parts hold the segment's first and last tile
+    const int c0 = line.owner(walk.pos - walk.tile);
+    const int n = line.owner(walk.pos - walk.tile + walk.span.tiles - 1) - c0 + 1;
+    // the joint reads them by bulk copies
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    end_sync();
+    if (tid == 0) {
+      int* counter = reinterpret_cast<int*>(a.ws + kAttnTicketsAt) + c0;
+      __threadfence();  // the partial result, which the barrier put before this, before the count
+      const bool last = atomicAdd(counter, 1) == n - 1;
+      __threadfence();
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      if (last) *counter = 0;
+      ctl->last = last;
+    }
+    end_sync();
+    if (ctl->last) {
+      joints[1] = Joint{c0, n, heads, row};
+      if (n_joints++ == 0) joints[0] = joints[1];
+    }
   }
-  if (timed_out && lane == 0) report_timeout_flag(a.table.status_flags, 41);
+  // The ring is free by now: every tile has been used.  (A part has at most two segments that it shares.)
+  int round = 0;
+#pragma unroll 1
+  for (int i = 0; i < n_joints; ++i)
+    if (!join_partials<S>(a, reinterpret_cast<const float*>(a.ws + kAttnPartialsAt), i == 0 ? joints[0] : joints[1], smem,
+                          int(S::kExpsAt), tid, &ctl->merge_full, round, &ctl->abort))
+      timed_out = true;
+  if (timed_out && lane == 0) report_timeout_flag(a.table.status_flags, 43);
 }
 
 // -------------------------------------------------------------------------- host ------------
 
-// [n_pages, heads, page, dim] rows, boxes of `box` tokens of one head of one page and `span` bytes.
-bool cache_map(CUtensorMap* map, const void* base, const CacheDev& c, int box, int span) {
+// A map of the cache's rows, [n_pages * heads * page, dim], for boxes of `box` rows.  Where a row is a
+// whole number of swizzled spans, a box holds all of them, span after span (`spans` of them, those past
+// the row's end as zeros); else a box is one span wide (and what lies past the row's end is zeros).
+bool cache_map(CUtensorMap* map, const void* base, const CacheDev& c, int box, int span, int spans) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t elem = c.e4m3 ? 1 : 2;
-  const cuuint64_t dims[4] = {cuuint64_t(c.dim), cuuint64_t(c.page), cuuint64_t(c.heads), cuuint64_t(c.n_pages)};
-  const cuuint64_t strides[3] = {c.dim * elem, cuuint64_t(c.page) * c.dim * elem,
-                                 cuuint64_t(c.heads) * c.page * c.dim * elem};
-  const cuuint32_t boxes[4] = {cuuint32_t(span / elem), cuuint32_t(box), 1, 1};
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
-  return fn(map, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+  const cuuint64_t elem = c.e4m3 ? 1 : 2, row = c.dim * elem;
+  const cuuint64_t dims[3] = {spans > 1 ? span / elem : cuuint64_t(c.dim),
+                              cuuint64_t(c.n_pages) * c.heads * c.page, spans > 1 ? row / span : 1};
+  const cuuint64_t strides[2] = {row, cuuint64_t(span)};
+  const cuuint32_t boxes[3] = {cuuint32_t(span / elem), cuuint32_t(box), cuuint32_t(spans)};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return fn(map, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
             dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
             span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -790,30 +1141,43 @@ int sm_count() {
 template <typename S>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   const CacheDev& c = a.cache;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(k_attn_decode<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
+  static const cudaError_t attr = [] {
+    cudaFuncAttributes f;
+    cudaError_t e = cudaFuncGetAttributes(&f, k_attn_decode<S>);
+    if (e != cudaSuccess) return e;
+    // the warpgroups divide up what the launch gets: with less than they ask for they would wait for ever
+    if (4 * f.numRegs < 2 * kComputeRegs + kProducerRegs + kEndRegs) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(k_attn_decode<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
+  }();
   if (attr != cudaSuccess) return attr;
   // tokens a copy: the largest power of two that divides a page, up to a tile
   const int box = std::min(S::kTokens, c.page & -c.page);
+  const int spans = c.dim % S::kSpanElems == 0 ? S::kSpans : 1;  // of a row in one copy
   CUtensorMap mk, mv;
-  if (!cache_map(&mk, c.k, c, box, S::kSpan) || !cache_map(&mv, c.v, c, box, S::kSpan)) return cudaErrorInvalidValue;
-  const int group = a.n_heads / c.heads;
+  if (!cache_map(&mk, c.k, c, box, S::kSpan, spans) || !cache_map(&mv, c.v, c, box, S::kSpan, spans))
+    return cudaErrorInvalidValue;
+  const int group = a.n_heads / c.heads, page_boxes = c.page / box;
+  // i / page_boxes = the high half of i * page_magic, for i below 2^32 / page_boxes: positions below 2^28
+  // make at most 2^24 boxes of 16, and a page at most 256
+  const uint32_t page_magic = uint32_t(((uint64_t(1) << 32) + page_boxes - 1) / page_boxes);
   return launch_pdl(k_attn_decode<S>, dim3(std::min(sm_count(), kMaxCtas)), dim3(kThreads), S::kSmem, s, a, mk, mv, box,
-                    group, (group + S::kHeads - 1) / S::kHeads);
+                    S::kSpans / spans, page_boxes, page_magic, group, (group + S::kHeads - 1) / S::kHeads);
 }
 
-// The kernel for a cache and group.  Blocks of 16 query heads where a group is larger than 8: a
-// second pass over the keys and values costs more than the wider products.  Not at widths above
-// 128, where 16 heads' accumulators do not fit the registers.
+// The kernel for a cache and a group of query heads: the heads of a segment are the fewest that hold
+// the group, up to 16 (a second pass over the keys and values costs more than the wider products),
+// and up to 8 at widths above 128, where 16 heads' accumulators do not fit the registers.
 template <typename F>
 auto with_shape(const CacheDev& c, int group, F f) {
-  auto by_type = [&](auto e4m3) {
-    constexpr bool E = decltype(e4m3)::value;
-    if (c.dim <= 64) return group <= 8 ? f(Shape<E, 64, 1>{}) : f(Shape<E, 64, 2>{});
-    if (c.dim <= 128) return group <= 8 ? f(Shape<E, 128, 1>{}) : f(Shape<E, 128, 2>{});
-    return f(Shape<E, 256, 1>{});
-  };
-  return c.e4m3 ? by_type(std::true_type{}) : by_type(std::false_type{});
+  if (c.e4m3) {
+    if (c.dim <= 64) return group <= 4 ? f(Shape<true, 64, 4>{}) : group <= 8 ? f(Shape<true, 64, 8>{}) : f(Shape<true, 64, 16>{});
+    if (c.dim <= 128)
+      return group <= 4 ? f(Shape<true, 128, 4>{}) : group <= 8 ? f(Shape<true, 128, 8>{}) : f(Shape<true, 128, 16>{});
+    return group <= 4 ? f(Shape<true, 256, 4>{}) : f(Shape<true, 256, 8>{});
+  }
+  if (c.dim <= 64) return group <= 8 ? f(Shape<false, 64, 8>{}) : f(Shape<false, 64, 16>{});
+  if (c.dim <= 128) return group <= 8 ? f(Shape<false, 128, 8>{}) : f(Shape<false, 128, 16>{});
+  return f(Shape<false, 256, 8>{});
 }
 
 }  // namespace

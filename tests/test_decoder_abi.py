@@ -26,7 +26,7 @@ def desc(moe, **kw):
 BAD_CACHES = [(dict(n_pages=0), -1), (dict(page_size=0), -1), (dict(page_size=24), -2), (dict(page_size=8192), -2),
               (dict(head_dim=0), -1), (dict(head_dim=72), -2), (dict(head_dim=272), -2), (dict(n_kv_heads=0), -1),
               (dict(dtype=0), -1), (dict(dtype=3), -1), (dict(k=0), -1), (dict(v=P + 8), -1), (dict(k_exp=0), -1),
-              (dict(v_exp=P + 4), -1)]
+              (dict(v_exp=P + 4), -1), (dict(n_pages=1 << 25), -2), (dict(n_kv_heads=1025), -2)]
 
 
 @pytest.mark.parametrize("bad,status", BAD_CACHES)
@@ -65,7 +65,7 @@ def test_kv_read_refusals(moe, at, value, status):
 
 @pytest.mark.parametrize("at,value,status", [
     (1, None, -1), (1, P + 4, -1), (2, 2047, -1), (2, 2052, -1), (3, 18, -1), (3, 0, -1), (3, 2048, -2), (4, -1, -1),
-    (4, 70000, -2), (5, None, -1), (5, P + 1, -1), (6, None, -1), (7, 0, -1), (7, 1 << 27, -2), (8, math.nan, -1),
+    (4, 70000, -2), (5, None, -1), (5, P + 1, -1), (6, None, -1), (7, 0, -1), (7, 1 << 27, -2), (7, (1 << 24) + 1, -2), (8, math.nan, -1),
     (8, math.inf, -1), (9, -1, -1), (10, None, -1), (10, P + 2, -1), (11, P + 1, -1), (12, None, -1), (13, 4096, -3)])
 def test_attn_decode_refusals(moe, at, value, status):
     args = [desc(moe), P, 2048, 16, 4, P, P, 8, 0.1, 0, P, None, WS, BIG, None]

@@ -243,6 +243,56 @@ def test_attention_split_long_rows(moe, e4m3):
     check_attention(moe, 4, [40 + 7 * i for i in range(70)], 4, 2, 64, 32, e4m3)
 
 
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 8, 8), (128, 16, 8), (128, 80, 8), (256, 8, 4)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_many_tiles_a_cta(moe, dim, heads, kv_heads, e4m3):
+    """Tens of tiles and several segments for every CTA: the ring goes round many times, and the page
+    table is read far past its first entries.  The 64-bit form is gathered on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(dim + heads)
+    page, B = 64, 7
+    lens = torch.tensor([9000, 12000, 8123, 1, 0, 11111, 6400], dtype=torch.int32)
+    width = 12000 // page + 1
+    n_pages = B * width
+    shape = (n_pages, kv_heads, page, dim)
+    pools = [torch.randn(shape, generator=g, device="cuda").to(BF) for _ in range(2)]
+    exps = [None, None]
+    if e4m3:
+        pools = [(32 * x.float()).to(torch.float8_e4m3fn).view(torch.uint8) for x in pools]
+        exps = [torch.randint(120, 125, shape[:3], generator=g, device="cuda").to(torch.uint8) for _ in range(2)]
+    cache = moe.KVCache(*pools, *exps)
+    table = torch.randperm(n_pages, generator=g, device="cuda").view(B, width).int()
+    q = torch.randn(B, heads, dim, generator=g, device="cuda").to(BF)
+    ws = moe.attn_workspace(cache, heads, B)
+    lse = torch.empty(B, heads, device="cuda")
+    outs = [moe.attn_decode(q, cache, lens.cuda(), table, ws, lse=lse) for _ in range(5)]
+    assert moe.get_status(ws) == 0
+    for out in outs[1:]:
+        assert torch.equal(out, outs[0])
+    scale = dim ** -0.5
+    for b, n in enumerate(lens.tolist()):
+        if n == 0:
+            assert not outs[0][b].any() and (lse[b] == -math.inf).all()
+            continue
+        at = torch.arange(n, device="cuda")
+        pg, row = table[b].long()[at // page], at % page
+        k, v = (x.permute(0, 2, 1, 3)[pg, row] for x in pools)
+        if e4m3:
+            k, v = (x.view(torch.float8_e4m3fn).double() * torch.exp2(e.permute(0, 2, 1)[pg, row].double() - 127)[..., None]
+                    for x, e in zip((k, v), exps))
+        else:
+            k, v = k.double(), v.double()
+        qh = q[b].double().view(kv_heads, heads // kv_heads, dim)
+        s = torch.einsum("kgd,nkd->kgn", qh, k) * scale
+        p = torch.softmax(s, -1)
+        want = torch.einsum("kgn,nkd->kgd", p, v)
+        size = (torch.einsum("kgd,nkd->kgn", qh.abs(), k.abs()).amax(-1) * scale)[..., None]
+        eps = (2 * dim + 6) * o.U32 * size + 4 * o.U32 * (2 + n / 16)
+        tol = o.UBF * want.abs() + (1 + o.UBF) * (o.UBF + 2 * eps + 2 * o.U32 * (n + 8)) * torch.einsum("kgn,nkd->kgd", p, v.abs())
+        close(outs[0][b].view_as(want), want.cpu(), tol.cpu(), f"sequence {b}")
+        want_lse = torch.logsumexp(s, -1)
+        close(lse[b].view_as(want_lse), want_lse.cpu(), (eps[..., 0] + 2 * o.U32 * n + 4 * o.U32 * want_lse.abs()).cpu(), f"lse {b}")
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_attention_sharp_and_scaled_rows(moe, e4m3):
     """Scores far apart (single tokens take all), a negative scale, a zero scale, row sizes over many
