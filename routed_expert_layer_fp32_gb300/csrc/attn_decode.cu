@@ -53,7 +53,7 @@ constexpr int kEndThreads = 128;
 constexpr int kThreads = kEndWarp * 32 + kEndThreads;
 // Registers a thread of the four warpgroups (compute twice, producers, segment ends); the launch gives
 // each 128, and the shares add up to that.
-constexpr int kComputeRegs = 168, kProducerRegs = 72, kEndRegs = 104;
+constexpr int kComputeRegs = 160, kProducerRegs = 80, kEndRegs = 112;
 static_assert(2 * kComputeRegs + kProducerRegs + kEndRegs <= 4 * (65536 / kThreads), "registers");
 constexpr size_t kSmemLimit = 227 * 1024;
 constexpr int kMaxCtas = 256;
@@ -71,9 +71,9 @@ struct Shape {
   static constexpr int kSpan = kRow < 128 ? kRow : 128;     // bytes of a row in one swizzled copy
   static constexpr int kSpans = kRow / kSpan;
   static constexpr int kSpanElems = kDim / kSpans;
-  // 32 KB stages (16 KB for the narrowest rows), 32 tokens a warp; 16 where the accumulators of two
-  // blocks of eight heads, or of wide rows, fill the registers
-  static constexpr int kPerWarp = !kE4M3 && kHeads * kDim > 1024 ? 16 : 32;
+  // 32 KB stages (16 KB for the narrowest rows); 16 or 32 tokens a warp, those of one product with the
+  // values
+  static constexpr int kPerWarp = kE4M3 ? 32 : 16;
   static constexpr int kTokens = kRow <= 128 ? 128 : 128 * 128 / kRow;
   static constexpr int kGroupWarps = kTokens / kPerWarp;
   static constexpr int kGroups = kWarps / kGroupWarps;
@@ -1085,9 +1085,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     end_sync();
     if (tid == 0) {
       int* counter = reinterpret_cast<int*>(a.ws + kAttnTicketsAt) + c0;
-      __threadfence();  // the partial result, which the barrier put before this, before the count
-      const bool last = atomicAdd(counter, 1) == n - 1;
-      __threadfence();
+      // releases the partial result (which the barrier put before this) and acquires the others'
+      int before;
+      asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+      const bool last = before == n - 1;
       asm volatile("fence.proxy.async.global;" ::: "memory");
       if (last) *counter = 0;
       ctl->last = last;
@@ -1170,9 +1171,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 template <typename F>
 auto with_shape(const CacheDev& c, int group, F f) {
   if (c.e4m3) {
-    if (c.dim <= 64) return group <= 4 ? f(Shape<true, 64, 4>{}) : group <= 8 ? f(Shape<true, 64, 8>{}) : f(Shape<true, 64, 16>{});
-    if (c.dim <= 128)
-      return group <= 4 ? f(Shape<true, 128, 4>{}) : group <= 8 ? f(Shape<true, 128, 8>{}) : f(Shape<true, 128, 16>{});
+    if (c.dim <= 64) return group <= 4 ? f(Shape<true, 64, 4>{}) : f(Shape<true, 64, 8>{});
+    if (c.dim <= 128) return group <= 4 ? f(Shape<true, 128, 4>{}) : f(Shape<true, 128, 8>{});
     return group <= 4 ? f(Shape<true, 256, 4>{}) : f(Shape<true, 256, 8>{});
   }
   if (c.dim <= 64) return group <= 8 ? f(Shape<false, 64, 8>{}) : f(Shape<false, 64, 16>{});

@@ -12,6 +12,11 @@ import torch
 from . import binding as _b
 from .binding import MOE_BF16, MOE_E4M3, MOE_F32
 
+# A decode step calls these operators a few times a layer with microseconds of GPU work each, so what
+# the host spends on a call counts: each tensor is looked at once, and only with the cheap accessors.
+_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: 0.1 us, a torch.cuda.Stream 3 us
+
 
 class MoeKvCacheC(ctypes.Structure):
     _fields_ = [("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
@@ -47,6 +52,7 @@ class KVCache:
         self.c = MoeKvCacheC(self.n_pages, self.page_size, self.n_kv_heads, self.head_dim, self.dtype, _b._ptr(k),
                              _b._ptr(v), _b._ptr(k_exp), _b._ptr(v_exp))
         self.ref = ctypes.byref(self.c)
+        self.device = k.get_device()
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, dtype: int = MOE_BF16,
@@ -62,27 +68,50 @@ class KVCache:
         return cls(k, v, *(torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)))
 
 
-def _check_int32(t: torch.Tensor, name: str, dims: int):
-    if t.dtype != torch.int32 or t.dim() != dims:
-        raise ValueError(f"{name} is an int32 tensor of {dims} dimension{'s' if dims > 1 else ''}")
+def _misfit(name: str, t: torch.Tensor, what: str):
+    return ValueError(f"{name} is {what}, contiguous and on the cache's GPU; got {t.dtype} {list(t.shape)} on {t.device}")
 
 
-def _rows(t: torch.Tensor, name: str, heads: int, dim: int):
+def _int32(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise _misfit(name, t, f"int32 {list(shape)}")
+    return t.data_ptr()
+
+
+def _table(t: torch.Tensor, dev: int):
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.get_device() != dev or not t.is_contiguous():
+        raise _misfit("page_table", t, "int32 [sequences, pages]")
+    n, width = t.shape
+    return t.data_ptr(), n, width
+
+
+def _workspace(ws: torch.Tensor, dev: int):
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise _misfit("ws", ws, "uint8")
+    return ws.data_ptr(), ws.numel()
+
+
+def _rows(t: torch.Tensor, name: str, T: int, heads: int, dim: int, dev: int):
     """(address, row stride) of [T, heads, dim] rows that are contiguous in themselves."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} is [tokens, {heads}, {dim}]")
-    if not t.is_cuda:
-        raise ValueError("libmoe takes CUDA tensors")
+    if t.shape != (T, heads, dim) or t.get_device() != dev:
+        raise ValueError(f"{name} is [{T}, {heads}, {dim}] on the cache's GPU; got {list(t.shape)} on {t.device}")
     s0, s1, s2 = t.stride()
     if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
         raise ValueError(f"{name}'s rows of [{heads}, {dim}] must be contiguous")
-    return t.data_ptr(), (s0 if t.shape[0] > 1 else heads * dim)
+    return t.data_ptr(), (s0 if T > 1 else heads * dim)
 
 
-def _on_one_device(t: torch.Tensor, others):
-    for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError("libmoe takes tensors of one device")
+def _full(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} is {list(shape)}, contiguous and on the same GPU; got {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _code(t: torch.Tensor, name: str) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} is bf16 or fp32, not {t.dtype}")
+    return code
 
 
 def attn_workspace(cache: KVCache, n_heads: int, B: int) -> torch.Tensor:
@@ -91,7 +120,7 @@ def attn_workspace(cache: KVCache, n_heads: int, B: int) -> torch.Tensor:
     if n == 0:
         raise _b.MoeError(-2, "moe_attn_workspace_bytes")
     ws = torch.empty(n, dtype=torch.uint8, device=cache.k.device)
-    _b._check(_b.lib().moe_attn_workspace_init(_b._ptr(ws), n, _b._stream()), "moe_attn_workspace_init")
+    _b._check(_b.lib().moe_attn_workspace_init(ws.data_ptr(), n, _raw_stream(cache.device)), "moe_attn_workspace_init")
     return ws
 
 
@@ -99,16 +128,18 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, pos: torch.Tensor
              ws: torch.Tensor, seq: Optional[torch.Tensor] = None) -> None:
     """Writes tokens' keys and values, k and v [T, n_kv_heads, head_dim] bf16 or fp32 (rows may be
     slices of a fused projection's output), at position pos[t] of sequence seq[t] (None: t)."""
-    T = k.shape[0]
-    if v.shape[0] != T or v.dtype != k.dtype:
-        raise ValueError("k and v have one length and type")
-    _check_tokens(T, pos, seq, page_table)
-    _on_one_device(cache.k, (k, v, pos, seq, page_table, ws))
-    kp, ks = _rows(k, "k", cache.n_kv_heads, cache.head_dim)
-    vp, vs = _rows(v, "v", cache.n_kv_heads, cache.head_dim)
-    _b._check(_b.lib().moe_kv_write(cache.ref, kp, vp, _b._dtype_code(k), ks, vs, T, _b._ptr(seq), _b._ptr(pos),
-                                    _b._ptr(page_table), page_table.shape[0], page_table.shape[1], _b._ptr(ws),
-                                    ws.numel(), _b._stream()), "moe_kv_write")
+    T, dev = k.shape[0], cache.device
+    code = _code(k, "k")
+    if v.dtype is not k.dtype:
+        raise ValueError("k and v have one type")
+    kp, ks = _rows(k, "k", T, cache.n_kv_heads, cache.head_dim, dev)
+    vp, vs = _rows(v, "v", T, cache.n_kv_heads, cache.head_dim, dev)
+    table, n_seqs, width = _table(page_table, dev)
+    wp, wn = _workspace(ws, dev)
+    rc = _b.lib().moe_kv_write(cache.ref, kp, vp, code, ks, vs, T, None if seq is None else _int32(seq, "seq", (T,), dev),
+                               _int32(pos, "pos", (T,), dev), table, n_seqs, width, wp, wn, _raw_stream(dev))
+    if rc:
+        raise _b.MoeError(rc, "moe_kv_write")
 
 
 def kv_read(cache: KVCache, pos: torch.Tensor, page_table: torch.Tensor, ws: torch.Tensor,
@@ -116,27 +147,21 @@ def kv_read(cache: KVCache, pos: torch.Tensor, page_table: torch.Tensor, ws: tor
             v: Optional[torch.Tensor] = None):
     """The keys and values at position pos[t] of sequence seq[t] (None: t): (k, v), each
     [T, n_kv_heads, head_dim] of `dtype`, or of the given output tensors."""
-    T = pos.shape[0]
+    T, dev = pos.shape[0], cache.device
     shape = (T, cache.n_kv_heads, cache.head_dim)
     k = k if k is not None else torch.empty(shape, dtype=dtype, device=cache.k.device)
     v = v if v is not None else torch.empty(shape, dtype=k.dtype, device=cache.k.device)
-    if k.shape != shape or v.shape != shape or k.dtype != v.dtype:
-        raise ValueError(f"k and v are {list(shape)} of one type")
-    _check_tokens(T, pos, seq, page_table)
-    _on_one_device(cache.k, (k, v, pos, seq, page_table, ws))
-    _b._check(_b.lib().moe_kv_read(cache.ref, T, _b._ptr(seq), _b._ptr(pos), _b._ptr(page_table), page_table.shape[0],
-                                   page_table.shape[1], _b._ptr(k), _b._ptr(v), _b._dtype_code(k), _b._ptr(ws),
-                                   ws.numel(), _b._stream()), "moe_kv_read")
+    code = _code(k, "k")
+    if v.dtype is not k.dtype:
+        raise ValueError("k and v have one type")
+    table, n_seqs, width = _table(page_table, dev)
+    wp, wn = _workspace(ws, dev)
+    rc = _b.lib().moe_kv_read(cache.ref, T, None if seq is None else _int32(seq, "seq", (T,), dev),
+                              _int32(pos, "pos", (T,), dev), table, n_seqs, width, _full(k, "k", shape, dev),
+                              _full(v, "v", shape, dev), code, wp, wn, _raw_stream(dev))
+    if rc:
+        raise _b.MoeError(rc, "moe_kv_read")
     return k, v
-
-
-def _check_tokens(T: int, pos, seq, page_table):
-    _check_int32(pos, "pos", 1)
-    _check_int32(page_table, "page_table", 2)
-    if seq is not None:
-        _check_int32(seq, "seq", 1)
-    if pos.shape[0] != T or (seq is not None and seq.shape[0] != T):
-        raise ValueError("pos and seq hold one entry a token")
 
 
 def attn_decode(q: torch.Tensor, cache: KVCache, lens: torch.Tensor, page_table: torch.Tensor, ws: torch.Tensor,
@@ -146,24 +171,27 @@ def attn_decode(q: torch.Tensor, cache: KVCache, lens: torch.Tensor, page_table:
     fused projection's output) over the last `window` (0: all) of lens[b] cached tokens.  scale
     defaults to head_dim ** -0.5.  Returns out [B, n_heads, head_dim] bf16; lse [B, n_heads] fp32,
     where given, receives the log-sum-exp of the scores."""
-    if q.dim() != 3 or q.dtype != torch.bfloat16:
+    if q.dim() != 3 or q.dtype is not torch.bfloat16:
         raise ValueError("q is [sequences, n_heads, head_dim] bf16")
-    B, H = q.shape[0], q.shape[1]
-    qp, qs = _rows(q, "q", H, cache.head_dim)
-    _check_int32(lens, "lens", 1)
-    _check_int32(page_table, "page_table", 2)
-    if lens.shape[0] != B or page_table.shape[0] != B:
-        raise ValueError("lens and page_table hold one row a sequence")
-    out = out if out is not None else torch.empty((B, H, cache.head_dim), dtype=torch.bfloat16, device=q.device)
-    if out.shape != q.shape or out.dtype != torch.bfloat16:
-        raise ValueError("out is [sequences, n_heads, head_dim] bf16")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, H)):
-        raise ValueError("lse is [sequences, n_heads] fp32")
-    _on_one_device(cache.k, (q, lens, page_table, ws, out, lse))
-    _b._check(_b.lib().moe_attn_decode(cache.ref, qp, qs, H, B, _b._ptr(lens), _b._ptr(page_table),
-                                       page_table.shape[1], cache.head_dim ** -0.5 if scale is None else scale, window,
-                                       _b._ptr(out), _b._ptr(lse), _b._ptr(ws), ws.numel(), _b._stream()),
-              "moe_attn_decode")
+    dev, dim = cache.device, cache.head_dim
+    B, H, _ = shape = q.shape
+    qp, qs = _rows(q, "q", B, H, dim, dev)
+    lp = _int32(lens, "lens", (B,), dev)
+    table, n_seqs, width = _table(page_table, dev)
+    if n_seqs != B:
+        raise ValueError("page_table holds one row a sequence")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    elif out.dtype is not torch.bfloat16:
+        raise ValueError("out is bf16")
+    if lse is not None and lse.dtype is not torch.float32:
+        raise ValueError("lse is fp32")
+    wp, wn = _workspace(ws, dev)
+    rc = _b.lib().moe_attn_decode(cache.ref, qp, qs, H, B, lp, table, width, dim ** -0.5 if scale is None else scale,
+                                  window, _full(out, "out", shape, dev),
+                                  None if lse is None else _full(lse, "lse", (B, H), dev), wp, wn, _raw_stream(dev))
+    if rc:
+        raise _b.MoeError(rc, "moe_attn_decode")
     return out
 
 
@@ -177,37 +205,43 @@ def block_norm(residual: torch.Tensor, w_pre: Optional[torch.Tensor], y: Optiona
     defaults to `residual`, updated in place."""
     if residual.dim() != 2:
         raise ValueError("residual is [tokens, d]")
-    T, d = residual.shape
-    if y is not None and y.shape != residual.shape:
-        raise ValueError("y has the residual's shape")
-    for w, name in ((w_pre, "w_pre"), (w_post, "w_post")):
-        if w is not None and (w.dtype != torch.float32 or w.shape != (d,)):
-            raise ValueError(f"{name} is [d] fp32")
-    gp, gs = None, 0
+    T, d = shape = residual.shape
+    dev = residual.get_device()
+    if dev < 0:
+        raise ValueError("libmoe takes CUDA tensors")
+    code = _code(residual, "residual")
+    rp = _full(residual, "residual", shape, dev)
+    yp, y_code, post, pre, gp, gs, g_code, xp, x_code = None, 0, None, None, None, 0, 0, None, 0
+    if y is not None:
+        yp, y_code = _full(y, "y", shape, dev), _code(y, "y")
+    if w_post is not None:
+        post = _full(w_post, "w_post", (d,), dev)
+        if w_post.dtype is not torch.float32:
+            raise ValueError("w_post is fp32")
     if gate is not None:
-        if gate.shape != (d,) and gate.shape != (T, d):
-            raise ValueError("gate is [d] or [tokens, d]")
-        if not gate.is_cuda or (gate.stride(-1) != 1 and d > 1):
-            raise ValueError("gate's rows are contiguous on the GPU")
-        gp, gs = gate.data_ptr(), (gate.stride(0) if gate.dim() == 2 and T > 1 else 0)
-    r_out = residual_out if residual_out is not None else residual
-    if r_out.shape != residual.shape or r_out.dtype != residual.dtype:
-        raise ValueError("residual_out has the residual's shape and type")
-    if w_pre is None:
-        if out is not None:
-            raise ValueError("an output norm needs w_pre")
-    elif out is None:
-        out = torch.empty((T, d), dtype=x_dtype, device=residual.device)
-    elif out.shape != residual.shape:
-        raise ValueError("out has the residual's shape")
-    _on_one_device(residual, (w_pre, y, w_post, gate, r_out, out))
-    code = _b._dtype_code
-    if y is None and r_out is residual:
-        r_ptr = None  # the residual stays as it is
+        per_token = gate.dim() == 2
+        if gate.shape != (shape if per_token else (d,)) or gate.get_device() != dev or (gate.stride(-1) != 1 and d > 1):
+            raise ValueError("gate is [d] or [tokens, d], its rows contiguous and on the same GPU")
+        gp, g_code = gate.data_ptr(), _code(gate, "gate")
+        gs = gate.stride(0) if per_token and T > 1 else 0
+    if residual_out is None:
+        residual_out = residual
+        op = None if y is None else rp  # without y the residual stays as it is
     else:
-        r_ptr = _b._ptr(r_out)
-    _b._check(_b.lib().moe_block_norm(_b._ptr(y), MOE_F32 if y is None else code(y), _b._ptr(w_post), gp,
-                                      MOE_F32 if gate is None else code(gate), gs, alpha, _b._ptr(residual), r_ptr,
-                                      code(residual), _b._ptr(w_pre), _b._ptr(out), MOE_F32 if out is None else code(out),
-                                      T, d, eps, _b._stream()), "moe_block_norm")
-    return r_out, out
+        op = _full(residual_out, "residual_out", shape, dev)
+        if residual_out.dtype is not residual.dtype:
+            raise ValueError("residual_out has the residual's type")
+    if w_pre is not None:
+        pre = _full(w_pre, "w_pre", (d,), dev)
+        if w_pre.dtype is not torch.float32:
+            raise ValueError("w_pre is fp32")
+        if out is None:
+            out = torch.empty(shape, dtype=x_dtype, device=residual.device)
+        xp, x_code = _full(out, "out", shape, dev), _code(out, "out")
+    elif out is not None:
+        raise ValueError("an output norm needs w_pre")
+    rc = _b.lib().moe_block_norm(yp, y_code, post, gp, g_code, gs, alpha, rp, op, code, pre, xp, x_code, T, d, eps,
+                                 _raw_stream(dev))
+    if rc:
+        raise _b.MoeError(rc, "moe_block_norm")
+    return residual_out, out
