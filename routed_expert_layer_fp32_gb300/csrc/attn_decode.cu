@@ -1129,16 +1129,6 @@ bool cache_map(CUtensorMap* map, const void* base, const CacheDev& c, int box, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-  static const int sms = [] {
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
-  }();
-  return sms;
-}
-
 template <typename S>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   const CacheDev& c = a.cache;

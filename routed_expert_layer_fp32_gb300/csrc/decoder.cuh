@@ -2,6 +2,9 @@
 // attention that reads it (attn_decode.cu) and the norms between blocks (block_norm.cu).
 #pragma once
 
+#include <algorithm>
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
@@ -76,10 +79,20 @@ __device__ __forceinline__ void store_vec8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+inline int sm_count() {
+  static const int sms = [] {
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+  }();
+  return sms;
+}
+
 // Workspace of the attention: the status record, then the join counters and partial results of
 // attn_decode.cu.
 constexpr size_t kAttnTicketsAt = sizeof(DevStatus);
-constexpr int kAttnTickets = 4096;  // an upper bound of the attention grid
+constexpr int kAttnTickets = 1024;  // an upper bound of the attention grid
 constexpr size_t kAttnPartialsAt = kAttnTicketsAt + size_t(kAttnTickets) * 4;
 
 struct AttnArgs {

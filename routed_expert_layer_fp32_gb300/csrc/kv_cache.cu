@@ -2,9 +2,10 @@
 // exponent a row) and reading them back.
 //
 // Both are copies bound by memory: a row is one token's key or value of one kv head.  A group of
-// kLanes lanes takes the key row and the value row of one (token, head), eight elements a lane, so
-// that the loads of both rows are in flight together and a row's largest magnitude is a few
-// shuffles; consecutive groups take consecutive heads of a token (contiguous input rows).
+// kLanes lanes takes the key and value rows of kHeadsEach heads of one token, eight elements a lane of
+// each.  So the place in the cache, three dependent loads away (sequence and position, then page, then
+// row), is looked up once for four rows, and four rows' loads are in flight together in every lane; a
+// row's largest magnitude is a few shuffles.
 //
 // Exponent and codes: e is the smallest power with max|x| <= 448 * 2^e, taken from the maximum's
 // bits.  x * 2^-e is exact (a power of two, and far from fp32's limits), so the code is the only
@@ -14,21 +15,23 @@
 namespace moe {
 namespace {
 
-// Where row (token t, head h) lies in the cache, as a row index over [n_pages, heads, page]; -1 for
-// a skipped or refused token.
+constexpr int kHeadsEach = 2;
+
+// The row (an index over [n_pages, heads, page]) of token t and head 0 in the cache; -1 for a skipped
+// or refused token.  Head h's row is h * page further.
 __device__ __forceinline__ int64_t cache_row(const CacheDev& c, const PageTable& pt, const int32_t* seq,
-                                             const int32_t* pos, int t, int h) {
+                                             const int32_t* pos, int t) {
   const int p = __ldg(pos + t);
   const int s = seq ? __ldg(seq + t) : t;
   if (p < 0) return -1;
-  const int slot = p / c.page;
+  const int slot = unsigned(p) / unsigned(c.page);
   int page = -1;
   if (s >= 0 && s < pt.n_seqs && slot < pt.max_pages) page = __ldg(pt.pages + int64_t(s) * pt.max_pages + slot);
   if (page < 0 || page >= c.n_pages) {
     report_bad_page(pt.status_flags);
     return -1;
   }
-  return (int64_t(page) * c.heads + h) * c.page + (p - slot * c.page);
+  return int64_t(page) * c.heads * c.page + (p - slot * c.page);
 }
 
 template <int kLanes>
@@ -52,31 +55,39 @@ template <int kLanes, bool kE4M3, typename Src>
 __global__ void __launch_bounds__(256) k_kv_write(CacheDev c, PageTable pt, const Src* __restrict__ k,
                                                   const Src* __restrict__ v, int64_t k_stride, int64_t v_stride, int T,
                                                   const int32_t* __restrict__ seq, const int32_t* __restrict__ pos) {
-  const int64_t group = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / kLanes;
-  const int lane = threadIdx.x % kLanes;
-  const bool live = group < int64_t(T) * c.heads;
-  const int t = live ? int(group / c.heads) : 0, h = live ? int(group - int64_t(t) * c.heads) : 0;
-  const bool mine = live && lane * 8 < c.dim;
+  const int t = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  const int h0 = blockIdx.y * kHeadsEach, heads = min(kHeadsEach, c.heads - h0);
+  const bool mine = t < T && lane * 8 < c.dim;
   pdl_begin();
-  float kx[8] = {}, vx[8] = {};
-  if (mine) {
-    load_vec8(k + t * k_stride + h * c.dim + lane * 8, kx);
-    load_vec8(v + t * v_stride + h * c.dim + lane * 8, vx);
-  }
-  const int64_t row = live ? cache_row(c, pt, seq, pos, t, h) : -1;
-  if constexpr (kE4M3) {
-    const uint32_t ke = row_exponent(group_max8<kLanes>(kx)), ve = row_exponent(group_max8<kLanes>(vx));
-    if (row < 0) return;
-    if (mine) {
-      *reinterpret_cast<uint2*>(c.k + row * c.dim + lane * 8) = codes8(kx, inverse_exp_value(ke));
-      *reinterpret_cast<uint2*>(c.v + row * c.dim + lane * 8) = codes8(vx, inverse_exp_value(ve));
+  float kx[kHeadsEach][8], vx[kHeadsEach][8];
+#pragma unroll
+  for (int j = 0; j < kHeadsEach; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) kx[j][i] = vx[j][i] = 0.0f;
+    if (mine && j < heads) {
+      load_vec8(k + t * k_stride + (h0 + j) * c.dim + lane * 8, kx[j]);
+      load_vec8(v + t * v_stride + (h0 + j) * c.dim + lane * 8, vx[j]);
     }
-    if (lane == 0) c.k_exp[row] = uint8_t(ke);
-    if (lane == 1) c.v_exp[row] = uint8_t(ve);
-  } else {
-    if (row < 0 || !mine) return;
-    store_vec8(reinterpret_cast<__nv_bfloat16*>(c.k) + row * c.dim + lane * 8, kx);
-    store_vec8(reinterpret_cast<__nv_bfloat16*>(c.v) + row * c.dim + lane * 8, vx);
+  }
+  const int64_t row0 = t < T ? cache_row(c, pt, seq, pos, t) : -1;
+#pragma unroll
+  for (int j = 0; j < kHeadsEach; ++j) {
+    const int64_t row = row0 + int64_t(h0 + j) * c.page;
+    const bool write = row0 >= 0 && j < heads;
+    if constexpr (kE4M3) {
+      const uint32_t ke = row_exponent(group_max8<kLanes>(kx[j])), ve = row_exponent(group_max8<kLanes>(vx[j]));
+      if (!write) continue;
+      if (mine) {
+        *reinterpret_cast<uint2*>(c.k + row * c.dim + lane * 8) = codes8(kx[j], inverse_exp_value(ke));
+        *reinterpret_cast<uint2*>(c.v + row * c.dim + lane * 8) = codes8(vx[j], inverse_exp_value(ve));
+      }
+      if (lane == 0) c.k_exp[row] = uint8_t(ke);
+      if (lane == 1) c.v_exp[row] = uint8_t(ve);
+    } else {
+      if (!write || !mine) continue;
+      store_vec8(reinterpret_cast<__nv_bfloat16*>(c.k) + row * c.dim + lane * 8, kx[j]);
+      store_vec8(reinterpret_cast<__nv_bfloat16*>(c.v) + row * c.dim + lane * 8, vx[j]);
+    }
   }
 }
 
@@ -97,28 +108,47 @@ template <int kLanes, bool kE4M3, typename Dst>
 __global__ void __launch_bounds__(256) k_kv_read(CacheDev c, PageTable pt, int T, const int32_t* __restrict__ seq,
                                                  const int32_t* __restrict__ pos, Dst* __restrict__ k_out,
                                                  Dst* __restrict__ v_out) {
-  const int64_t group = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) / kLanes;
-  const int lane = threadIdx.x % kLanes;
-  if (group >= int64_t(T) * c.heads || lane * 8 >= c.dim) return;
-  const int t = int(group / c.heads), h = int(group - int64_t(t) * c.heads);
+  const int t = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  const int h0 = blockIdx.y * kHeadsEach, heads = min(kHeadsEach, c.heads - h0);
+  if (t >= T || lane * 8 >= c.dim) return;
   pdl_begin();
-  const int64_t row = cache_row(c, pt, seq, pos, t, h);
-  float kx[8] = {}, vx[8] = {};
-  if (row >= 0) {
+  const int64_t row0 = cache_row(c, pt, seq, pos, t);
+  float kx[kHeadsEach][8], vx[kHeadsEach][8];
+  uint2 kc[kHeadsEach], vc[kHeadsEach];
+  uint32_t ke[kHeadsEach], ve[kHeadsEach];
+#pragma unroll
+  for (int j = 0; j < kHeadsEach; ++j) {
+    const int64_t row = row0 + int64_t(h0 + j) * c.page;
+    const bool read = row0 >= 0 && j < heads;
     if constexpr (kE4M3) {
-      const uint2 kc = *reinterpret_cast<const uint2*>(c.k + row * c.dim + lane * 8);
-      const uint2 vc = *reinterpret_cast<const uint2*>(c.v + row * c.dim + lane * 8);
-      const uint32_t ke = c.k_exp[row], ve = c.v_exp[row];
-      values8(kc, exp_value(ke), kx);
-      values8(vc, exp_value(ve), vx);
+      kc[j] = vc[j] = make_uint2(0u, 0u);  // zeros for a token that is not there
+      ke[j] = ve[j] = kExpBias;
+      if (read) {
+        kc[j] = *reinterpret_cast<const uint2*>(c.k + row * c.dim + lane * 8);
+        vc[j] = *reinterpret_cast<const uint2*>(c.v + row * c.dim + lane * 8);
+        ke[j] = c.k_exp[row];
+        ve[j] = c.v_exp[row];
+      }
     } else {
-      load_vec8(reinterpret_cast<const __nv_bfloat16*>(c.k) + row * c.dim + lane * 8, kx);
-      load_vec8(reinterpret_cast<const __nv_bfloat16*>(c.v) + row * c.dim + lane * 8, vx);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) kx[j][i] = vx[j][i] = 0.0f;
+      if (read) {
+        load_vec8(reinterpret_cast<const __nv_bfloat16*>(c.k) + row * c.dim + lane * 8, kx[j]);
+        load_vec8(reinterpret_cast<const __nv_bfloat16*>(c.v) + row * c.dim + lane * 8, vx[j]);
+      }
     }
   }
-  const int64_t at = group * c.dim + lane * 8;
-  store_vec8(k_out + at, kx);
-  store_vec8(v_out + at, vx);
+#pragma unroll
+  for (int j = 0; j < kHeadsEach; ++j) {
+    if (j >= heads) continue;
+    if constexpr (kE4M3) {
+      values8(kc[j], exp_value(ke[j]), kx[j]);
+      values8(vc[j], exp_value(ve[j]), vx[j]);
+    }
+    const int64_t at = (int64_t(t) * c.heads + h0 + j) * c.dim + lane * 8;
+    store_vec8(k_out + at, kx[j]);
+    store_vec8(v_out + at, vx[j]);
+  }
 }
 
 // The lanes of a row: a power of two that covers it with eight elements each.
@@ -129,7 +159,9 @@ cudaError_t with_lanes(int dim, F f) {
   return f(std::integral_constant<int, 32>{});
 }
 
-unsigned group_blocks(int64_t groups, int lanes) { return unsigned((groups * lanes + 255) / 256); }
+dim3 token_grid(int T, int lanes, int heads) {
+  return dim3((T + 256 / lanes - 1) / (256 / lanes), (heads + kHeadsEach - 1) / kHeadsEach);
+}
 
 }  // namespace
 
@@ -138,7 +170,7 @@ cudaError_t launch_kv_write(const CacheDev& c, const PageTable& pt, const void* 
                             cudaStream_t s) {
   return with_lanes(c.dim, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    const dim3 grid(group_blocks(int64_t(T) * c.heads, L));
+    const dim3 grid = token_grid(T, L, c.heads);
     auto go = [&](auto e4m3, auto src) {
       using Src = decltype(src);
       return launch_pdl(k_kv_write<L, decltype(e4m3)::value, Src>, grid, dim3(256), 0, s, c, pt,
@@ -153,7 +185,7 @@ cudaError_t launch_kv_read(const CacheDev& c, const PageTable& pt, int T, const 
                            void* k_out, void* v_out, bool bf16, cudaStream_t s) {
   return with_lanes(c.dim, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    const dim3 grid(group_blocks(int64_t(T) * c.heads, L));
+    const dim3 grid = token_grid(T, L, c.heads);
     auto go = [&](auto e4m3, auto dst) {
       using Dst = decltype(dst);
       return launch_pdl(k_kv_read<L, decltype(e4m3)::value, Dst>, grid, dim3(256), 0, s, c, pt, T, seq, pos,
