@@ -308,7 +308,7 @@ moe_status moe_attn_workspace_init(void* ws, size_t ws_bytes, moe_stream_t strea
  *   lse[b,h] = log sum_j exp(scale q[b,h].k_j)
  *   q           B rows of [n_heads, head_dim] bf16, q_stride elements apart (a multiple of 8)
  *   lens        [B] int32 on the device; sequence b is row b of page_table [B, max_pages]
- *   out         [B, n_heads, head_dim] bf16
+ *   out         [B, n_heads, head_dim] bf16, not overlapping q
  *   lse         [B, n_heads] fp32 or NULL: joins this result with another part of the context
  * n <= 0 gives zeros and an lse of -infinity.  n beyond the page table is cut to it, and a page
  * outside [0, n_pages) is left out as if masked; both record MOE_ERR_BAD_PAGE.  What lies in the

@@ -294,6 +294,42 @@ def test_attention_many_tiles_a_cta(moe, dim, heads, kv_heads, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_many_short_sequences(moe, e4m3):
+    """More sequences than threads that count them, most of them short, many empty."""
+    g = gen(77)
+    lens = torch.randint(0, 40, (1500,), generator=g)
+    lens[torch.randperm(1500, generator=g)[:500]] = 0
+    lens[700], lens[1499] = 300, 171
+    check_attention(moe, 78, lens.tolist(), 2, 1, 64, 16, e4m3, poison=False)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_nan_stays_in_its_head(moe, e4m3):
+    """A query with a NaN or an infinity, and a key row with a NaN, spoil their heads and no other."""
+    g = gen(81)
+    pools = host_cache(g, 12, 2, 16, 64, e4m3)
+    table = tables(g, 2, 6, 12)
+    lens = torch.tensor([90, 33], dtype=torch.int32)
+    q = torch.randn(2, 8, 64, generator=g).to(BF)
+    want, _, tol, _ = o.attention(q, *pools, lens, table, 0.125, 0)
+    q[0, 1, 5], q[1, 6, 0] = math.nan, math.inf
+    p, r = o.place(16, table, 0, 37)
+    if e4m3:
+        pools[0][p, 1, r, 3] = 0x7F
+    else:
+        pools[0][p, 1, r, 3] = math.nan
+    cache = to_device(moe, pools)
+    ws = moe.attn_workspace(cache, 8, 2)
+    out = moe.attn_decode(q.cuda(), cache, lens.cuda(), table.cuda(), ws, scale=0.125)
+    spoilt = torch.zeros(2, 8, dtype=torch.bool)
+    spoilt[0, 1] = spoilt[1, 6] = True
+    spoilt[0, 4:] = True            # kv head 1 of sequence 0
+    assert torch.isnan(out.cpu()[spoilt]).all()
+    close(out.cpu()[~spoilt], want[~spoilt], tol[~spoilt], "the other heads")
+    assert moe.get_status(ws) == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_attention_sharp_and_scaled_rows(moe, e4m3):
     """Scores far apart (single tokens take all), a negative scale, a zero scale, row sizes over many
     powers of two, tiny and huge queries."""
