@@ -102,7 +102,8 @@ struct Shape {
   // layout: stages, exponents, queries, join buffer, control; 1 KB to align the stages
   static constexpr size_t kFixed = size_t(kSlots) * kQueries + size_t(kWarps) * kJoinWarp * 4 + sizeof(Control) + 1024;
   static constexpr int kRoom = int((kSmemLimit - kFixed) / (kStage + kExps));
-  static constexpr int kStages = kRoom < 192 * 1024 / kStage ? kRoom : 192 * 1024 / kStage;
+  // a multiple of the groups: each has as many stages as the others
+  static constexpr int kStages = (kRoom < 192 * 1024 / kStage ? kRoom : 192 * 1024 / kStage) / kGroups * kGroups;
   static constexpr size_t kExpsAt = size_t(kStages) * kStage;
   static constexpr size_t kQueriesAt = kExpsAt + size_t(kStages) * kExps;
   static constexpr size_t kJoinAt = kQueriesAt + size_t(kSlots) * kQueries;
@@ -1163,7 +1164,7 @@ auto with_shape(const CacheDev& c, int group, F f) {
   if (c.e4m3) {
     if (c.dim <= 64) return group <= 4 ? f(Shape<true, 64, 4>{}) : f(Shape<true, 64, 8>{});
     if (c.dim <= 128) return group <= 4 ? f(Shape<true, 128, 4>{}) : f(Shape<true, 128, 8>{});
-    return group <= 4 ? f(Shape<true, 256, 4>{}) : f(Shape<true, 256, 8>{});
+    return f(Shape<true, 256, 4>{});
   }
   if (c.dim <= 64) return group <= 8 ? f(Shape<false, 64, 8>{}) : f(Shape<false, 64, 16>{});
   if (c.dim <= 128) return group <= 8 ? f(Shape<false, 128, 8>{}) : f(Shape<false, 128, 16>{});
