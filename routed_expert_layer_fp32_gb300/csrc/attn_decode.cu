@@ -20,19 +20,26 @@
 // accumulator) in the workspace, and the CTA that writes the last of them (a counter a segment,
 // back to 0 afterwards) joins them in CTA order, so the result does not depend on timing.
 //
-// In a CTA, a warp is the producer: it looks up pages and starts the tiles' TMA copies into a ring of
+// In a CTA, two warps are producers: they look up pages and start the tiles' TMA copies into a ring of
 // shared-memory stages.  Another lays the next segments' queries out as operands.  Eight warps
 // compute, in groups that take the tiles in turn; a warp has kPerWarp tokens of each of its group's
 // tiles and its own m, sum and accumulator, and at a segment's end leaves them in shared memory and
 // goes on.  Four warps add the eight results up, write the output or the partial result, and join
 // partial results.  So neither the copies nor the products wait for a segment's end (with all of that
-// in the eight warps, a segment cost 3.5 us next to 3 us of products at 513 tokens).  A stage belongs
-// to one group: a barrier's wait tells only the parity of the phase, so whoever waits for a stage has
-// to have seen each of its phases.
+// in the eight warps, 128 windows of 513 tokens took 31.4 us, like this 22.7).  A stage belongs to one
+// group: a barrier's wait tells only the parity of the phase, so whoever waits for a stage has to have
+// seen each of its phases.
 //
-// Starting a copy holds a warp up for 100 to 200 cycles, which is enough time for two warps to fall
-// behind the memory with the 2 KB copies of 16-token pages if they compute anything else there: no
-// division a tile, and each lane has its own copy of every tile worked out beforehand.
+// Starting a copy holds a warp up for 100 to 200 cycles, enough to fall behind the memory with the 2 KB
+// copies of 16-token pages if it computes anything else there: there is no division a tile, each lane
+// has its own copy of every tile worked out beforehand, and the copies of a tile are shared out between
+// the two warps (32 mixed lengths, E4M3: one warp 22.8 us, two 20.8).
+//
+// Measured (GB300, bf16 unless said, 4 kv heads of 4 query heads, 128 wide): 64 sequences of up to 16k
+// tokens 200 us, 1.37 GB at the measured copy rate; one of 64k tokens 28.9 us (69 % of that rate); one
+// 513-token window 6.8 us, all of it latency (the lengths, the pages, the tile, the count of partial
+// results and their joint are each a trip to memory).  What a call costs beyond its bytes is about
+// 10 us: 3 to 4 until the first tile is there, 4 from the last tile to the end, and the launch.
 //
 // The products are warp MMAs with the tokens (scores) and the value elements (output) on the M
 // side and the query heads on the N side, so that eight columns are the unit that a small group is
@@ -160,6 +167,22 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort) {
   return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort);
 }
+// The same for what takes as long as a CTA's part of a segment does, which a call over the whole memory
+// can stretch past mbar_wait's limit; a CTA that is stuck sets `abort` long before.
+constexpr unsigned long long kPartLimitNs = 5ull * 1000 * 1000 * 1000;
+__device__ __forceinline__ bool wait_part(uint64_t* bar, uint32_t parity, int* abort) {
+  const unsigned long long t0 = global_timer_ns();
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 63u) {
+      if (*static_cast<volatile int*>(abort)) return false;
+      if (global_timer_ns() - t0 > kPartLimitNs) {
+        *static_cast<volatile int*>(abort) = 1;
+        return false;
+      }
+    }
+  }
+}
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -200,7 +223,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
   return s;
 }
 
-// Walks a CTA's part of the line, segment by segment.  Producer and consumers walk alike.
+// Walks a CTA's part of the line, segment by segment.
 template <typename S>
 struct Walk {
   int b, seg, tile;  // sequence, segment in it, first tile (of the segment's) that is ours
@@ -231,7 +254,6 @@ struct Walk {
     take = min(span.tiles, hi - pos);
   }
   __device__ __forceinline__ bool whole() const { return take == span.tiles; }  // the segment is all ours
-  __device__ __forceinline__ bool last() const { return pos + take == hi; }
 };
 
 // The line cut into the CTAs' parts: the first `more` have one tile more than the others.
@@ -945,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- queries -------------
       for (; !walk.done(); walk.next(a, segs), ++seg) {
         const int kv = walk.seg / head_blocks, hb = walk.seg % head_blocks, slot = seg % S::kSlots;
-        if (!__all_sync(0xffffffffu, wait(&ctl->q_empty[slot], ((seg / S::kSlots) & 1) ^ 1, &ctl->abort))) {
+        if (!__all_sync(0xffffffffu, wait_part(&ctl->q_empty[slot], ((seg / S::kSlots) & 1) ^ 1, &ctl->abort))) {
           if (lane == 0) report_timeout_flag(a.table.status_flags, 41);
           break;
         }
@@ -999,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tv.valid = ctl->valid[stage] >> (row0 / 16) & kAll;
         if (tv.valid == kAll && tv.pos0 >= tv.first && tv.pos0 + S::kPerWarp <= tv.end)
           mine_w.template tile<true>(tv);
-        else if (tv.valid != 0)
+        else if (tv.valid != 0 && tv.pos0 < tv.end && tv.pos0 + S::kPerWarp > tv.first)
           mine_w.template tile<false>(tv);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->empty[stage]);
@@ -1030,14 +1052,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int kv = walk.seg / head_blocks, hb = walk.seg % head_blocks;
     const int heads = min(S::kHeads, group - hb * S::kHeads);
     const int64_t row = int64_t(walk.b) * a.n_heads + kv * group + hb * S::kHeads;  // of the first head in out
-    const bool whole = walk.take == walk.span.tiles;  // finished here, or a partial result
+    const bool whole = walk.whole();  // finished here, or a partial result
     float* slots = reinterpret_cast<float*>(a.ws + kAttnPartialsAt);
     // slot 0: a segment that began before this CTA's part; slot 1: one that begins in it
     float* slot = slots + (size_t(blockIdx.x) * 2 + (walk.tile == 0)) * S::kSlot;
 
     // -------- the warps' results --------
     for (int d0 = 0; d0 < c.dim; d0 += S::kPassDim, ++joins) {
-      if (!wait(&ctl->join_full, joins & 1, &ctl->abort)) timed_out = true;
+      if (!wait_part(&ctl->join_full, joins & 1, &ctl->abort)) timed_out = true;
       constexpr int kVecs = S::kPassDim / 4;
       for (int i = tid; i < heads * kVecs; i += kEndThreads) {
         const int h = i / kVecs, d = (i % kVecs) * 4;
@@ -1156,9 +1178,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
                     S::kSpans / spans, page_boxes, page_magic, group, (group + S::kHeads - 1) / S::kHeads);
 }
 
-// The kernel for a cache and a group of query heads: the heads of a segment are the fewest that hold
-// the group, up to 16 (a second pass over the keys and values costs more than the wider products),
-// and up to 8 at widths above 128, where 16 heads' accumulators do not fit the registers.
+// The kernel for a cache and a group of query heads: a segment's heads are the fewest that hold the
+// group, and of a larger group as many as its registers do.
+//   bf16: up to 16 (groups of 16, 64 x 8k tokens: 66 us, in two passes of 8 99; small calls, whose time
+//   is the joint of the partial results, lose: 8 x 8k 21 against 16), 8 at widths above 128.
+//   E4M3: up to 8 (16 spill: 29.3 us against 16.7 in two passes; a group of 8 in one pass 70 us, in two of
+//   4 108), 4 at widths above 128 (8 spill: 39.0 against 28.6).
 template <typename F>
 auto with_shape(const CacheDev& c, int group, F f) {
   if (c.e4m3) {

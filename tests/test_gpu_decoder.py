@@ -243,15 +243,12 @@ def test_attention_split_long_rows(moe, e4m3):
     check_attention(moe, 4, [40 + 7 * i for i in range(70)], 4, 2, 64, 32, e4m3)
 
 
-@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 8, 8), (128, 16, 8), (128, 80, 8), (256, 8, 4)])
-@pytest.mark.parametrize("e4m3", [False, True])
-def test_attention_many_tiles_a_cta(moe, dim, heads, kv_heads, e4m3):
-    """Tens of tiles and several segments for every CTA: the ring goes round many times, and the page
-    table is read far past its first entries.  The 64-bit form is gathered on the GPU."""
+def check_dense(moe, dim, heads, kv_heads, e4m3, lens):
+    """Long sequences against a 64-bit form gathered on the GPU."""
     g = torch.Generator(device="cuda").manual_seed(dim + heads)
-    page, B = 64, 7
-    lens = torch.tensor([9000, 12000, 8123, 1, 0, 11111, 6400], dtype=torch.int32)
-    width = 12000 // page + 1
+    page, B = 64, len(lens)
+    width = max(lens) // page + 1
+    lens = torch.tensor(lens, dtype=torch.int32)
     n_pages = B * width
     shape = (n_pages, kv_heads, page, dim)
     pools = [torch.randn(shape, generator=g, device="cuda").to(BF) for _ in range(2)]
@@ -291,6 +288,22 @@ def test_attention_many_tiles_a_cta(moe, dim, heads, kv_heads, e4m3):
         close(outs[0][b].view_as(want), want.cpu(), tol.cpu(), f"sequence {b}")
         want_lse = torch.logsumexp(s, -1)
         close(lse[b].view_as(want_lse), want_lse.cpu(), (eps[..., 0] + 2 * o.U32 * n + 4 * o.U32 * want_lse.abs()).cpu(), f"lse {b}")
+
+
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 8, 8), (128, 16, 8), (128, 80, 8), (256, 8, 4)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_many_tiles_a_cta(moe, dim, heads, kv_heads, e4m3):
+    """Tens of tiles and several segments for every CTA: the ring goes round many times, and the page
+    table is read far past its first entries."""
+    check_dense(moe, dim, heads, kv_heads, e4m3, [9000, 12000, 8123, 1, 0, 11111, 6400])
+
+
+@pytest.mark.parametrize("dim,heads", [(64, 16), (128, 16), (128, 8), (256, 8), (256, 3)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_one_row_over_all_ctas(moe, dim, heads, e4m3):
+    """One sequence and kv head cut between all CTAs: more partial results than the last of them has room
+    to hold at once."""
+    check_dense(moe, dim, heads, 1, e4m3, [40000])
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
