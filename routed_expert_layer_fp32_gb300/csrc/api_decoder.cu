@@ -176,6 +176,7 @@ moe_status moe_block_norm(const void* y, moe_dtype y_dtype, const float* w_post,
   a.gate_stride = gate_stride;
   a.alpha = alpha;
   a.eps = eps;
+  a.inv_d = 1.0f / float(d);
   a.residual = residual;
   a.residual_out = residual_out;
   a.w_pre = w_pre;

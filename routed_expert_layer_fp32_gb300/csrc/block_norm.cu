@@ -6,7 +6,7 @@
 // thread), so y and the residual are read once and both results written once.  What bounds it is
 // memory, and with more rows than CTAs fit on the GPU each CTA walks rows and loads its next one before
 // it works on the current one, so that the two sums over the row, each a barrier, do not leave the
-// memory idle (16384 rows of 2048 bf16: 46.1 us, 86 % of the measured copy rate; one row a CTA 62.6;
+// memory idle (16384 rows of 2048 bf16: 44.8 us, 88 % of the measured copy rate; one row a CTA 62.6;
 // two rows ahead 47.3).  The sums of squares are fp32: over a thread's elements, then the warp's lanes,
 // then the warps in order (the result does not depend on scheduling).
 #include "decoder.cuh"
@@ -52,7 +52,7 @@ struct Raw8 {
 };
 
 // Threads that fit an SM: 64 registers hold one or two groups of eight with the next row's (with 42
-// registers and 1536 threads the 16384 x 2048 case takes 60.5 us against 46.1).
+// registers and 1536 threads the 16384 x 2048 case took 60.5 us against 46.1).
 constexpr int kResident = 1024;
 
 template <int kVecs, typename Y, typename R, typename X>
@@ -67,11 +67,14 @@ __global__ void __launch_bounds__(kResident, 1) k_block_norm(NormArgs a) {
   pdl_begin();
   Raw8<Y> y_next[kVecs];
   Raw8<R> r_next[kVecs];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {  // zeros stay where a thread has no elements, or there is no y
+    y_next[j].clear();
+    r_next[j].clear();
+  }
   auto fetch = [&](int row) {
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      y_next[j].clear();
-      r_next[j].clear();
       if (c0 + j * step >= a.d) continue;
       const int64_t at = int64_t(row) * a.d + c0 + j * step;
       r_next[j].load(residual + at);
@@ -90,14 +93,14 @@ __global__ void __launch_bounds__(kResident, 1) k_block_norm(NormArgs a) {
     }
     if (row + gridDim.x < a.T) fetch(row + gridDim.x);
     if (y) {
-      float post = 1.0f;
+      float scale = a.alpha;  // times the post-norm's 1 / rms
       if (a.w_post) {
         float s = 0.0f;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j)
 #pragma unroll
           for (int i = 0; i < 8; ++i) s += z[j][i] * z[j][i];
-        post = rsqrtf(block_sum(s, part[turn]) / float(a.d) + a.eps);
+        scale *= rsqrtf(fmaf(block_sum(s, part[turn]), a.inv_d, a.eps));
       }
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) {
@@ -107,7 +110,7 @@ __global__ void __launch_bounds__(kResident, 1) k_block_norm(NormArgs a) {
           float w[8];
           load_vec8(a.w_post + c, w);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[j][i] *= post * w[i];
+          for (int i = 0; i < 8; ++i) z[j][i] *= w[i];
         }
         if (a.gate) {
           float g[8];
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(kResident, 1) k_block_norm(NormArgs a) {
           for (int i = 0; i < 8; ++i) z[j][i] *= g[i];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[j][i] = fmaf(a.alpha, z[j][i], r[j][i]);
+        for (int i = 0; i < 8; ++i) r[j][i] = fmaf(scale, z[j][i], r[j][i]);
       }
     }
     if (a.residual_out) {
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(kResident, 1) k_block_norm(NormArgs a) {
     for (int j = 0; j < kVecs; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s += r[j][i] * r[j][i];
-    const float pre = rsqrtf(block_sum(s, part[turn + 1]) / float(a.d) + a.eps);
+    const float pre = rsqrtf(fmaf(block_sum(s, part[turn + 1]), a.inv_d, a.eps));
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       const int c = c0 + j * step;

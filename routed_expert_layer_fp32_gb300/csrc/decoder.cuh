@@ -121,7 +121,7 @@ struct NormArgs {
   const float* w_post;
   const void* gate;
   int64_t gate_stride;
-  float alpha, eps;
+  float alpha, eps, inv_d;
   const void* residual;
   void* residual_out;
   const float* w_pre;
