@@ -273,7 +273,8 @@ typedef struct {
  *             v_stride elements apart (a fused projection's output is taken as it lies); both a
  *             multiple of 16 bytes
  *   seq, pos  [T] int32: each token's sequence and position; seq NULL: token t is sequence t's.
- *             A negative position skips the token.  Two tokens at one place leave either's row.
+ *             A negative position skips the token.  Two tokens of one call must not be given one
+ *             place (its row is then undefined).
  * bf16 cache: values rounded to nearest even.  E4M3 cache: a row's exponent is the smallest power
  * of two (2^-127 at least) that brings its largest magnitude to 448 at most, and its codes are the
  * scaled values rounded to nearest even: scaling by a power of two is exact, so each value is

@@ -15,7 +15,8 @@ from .binding import MOE_BF16, MOE_E4M3, MOE_F32
 # A decode step calls these operators a few times a layer with microseconds of GPU work each, so what
 # the host spends on a call counts: each tensor is looked at once, and only with the cheap accessors.
 _CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: 0.1 us, a torch.cuda.Stream 3 us
+# the current stream's handle alone: 0.1 us, a torch.cuda.Stream 3 us (absent from builds without CUDA)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class MoeKvCacheC(ctypes.Structure):
@@ -69,49 +70,8 @@ class KVCache:
 
 
 def _misfit(name: str, t: torch.Tensor, what: str):
-    return ValueError(f"{name} is {what}, contiguous and on the cache's GPU; got {t.dtype} {list(t.shape)} on {t.device}")
-
-
-def _int32(t: torch.Tensor, name: str, shape, dev: int) -> int:
-    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise _misfit(name, t, f"int32 {list(shape)}")
-    return t.data_ptr()
-
-
-def _table(t: torch.Tensor, dev: int):
-    if t.dtype is not torch.int32 or t.dim() != 2 or t.get_device() != dev or not t.is_contiguous():
-        raise _misfit("page_table", t, "int32 [sequences, pages]")
-    n, width = t.shape
-    return t.data_ptr(), n, width
-
-
-def _workspace(ws: torch.Tensor, dev: int):
-    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
-        raise _misfit("ws", ws, "uint8")
-    return ws.data_ptr(), ws.numel()
-
-
-def _rows(t: torch.Tensor, name: str, T: int, heads: int, dim: int, dev: int):
-    """(address, row stride) of [T, heads, dim] rows that are contiguous in themselves."""
-    if t.shape != (T, heads, dim) or t.get_device() != dev:
-        raise ValueError(f"{name} is [{T}, {heads}, {dim}] on the cache's GPU; got {list(t.shape)} on {t.device}")
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
-        raise ValueError(f"{name}'s rows of [{heads}, {dim}] must be contiguous")
-    return t.data_ptr(), (s0 if T > 1 else heads * dim)
-
-
-def _full(t: torch.Tensor, name: str, shape, dev: int) -> int:
-    if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} is {list(shape)}, contiguous and on the same GPU; got {list(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _code(t: torch.Tensor, name: str) -> int:
-    code = _CODES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} is bf16 or fp32, not {t.dtype}")
-    return code
+    return ValueError(f"{name} must be {what}, on the same GPU as the others; got {t.dtype} {list(t.shape)} with strides "
+                      f"{list(t.stride())} on {t.device}")
 
 
 def attn_workspace(cache: KVCache, n_heads: int, B: int) -> torch.Tensor:
@@ -124,20 +84,49 @@ def attn_workspace(cache: KVCache, n_heads: int, B: int) -> torch.Tensor:
     return ws
 
 
+def _row_stride(t: torch.Tensor, name: str, heads: int, dim: int) -> int:
+    """Elements from one row [heads, dim] of t [T, heads, dim] to the next; the rows are contiguous in themselves."""
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
+        raise _misfit(name, t, f"rows of [{heads}, {dim}] that are contiguous in themselves")
+    return s0 if t.shape[0] > 1 else heads * dim
+
+
+def _tokens(pos, seq, page_table, ws, T: int, dev: int):
+    """Addresses of pos and seq (or None), and the page table's and the workspace's address and size."""
+    if pos.dtype is not torch.int32 or pos.shape != (T,) or pos.get_device() != dev or not pos.is_contiguous():
+        raise _misfit("pos", pos, f"int32 [{T}], contiguous")
+    sp = None
+    if seq is not None:
+        if seq.dtype is not torch.int32 or seq.shape != (T,) or seq.get_device() != dev or not seq.is_contiguous():
+            raise _misfit("seq", seq, f"int32 [{T}], contiguous")
+        sp = seq.data_ptr()
+    return (pos.data_ptr(), sp, *_table(page_table, ws, dev))
+
+
+def _table(page_table, ws, dev: int):
+    if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.get_device() != dev
+            or not page_table.is_contiguous()):
+        raise _misfit("page_table", page_table, "int32 [sequences, pages], contiguous")
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise _misfit("ws", ws, "uint8, contiguous")
+    n_seqs, width = page_table.shape
+    return page_table.data_ptr(), n_seqs, width, ws.data_ptr(), ws.numel()
+
+
 def kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, pos: torch.Tensor, page_table: torch.Tensor,
              ws: torch.Tensor, seq: Optional[torch.Tensor] = None) -> None:
     """Writes tokens' keys and values, k and v [T, n_kv_heads, head_dim] bf16 or fp32 (rows may be
     slices of a fused projection's output), at position pos[t] of sequence seq[t] (None: t)."""
-    T, dev = k.shape[0], cache.device
-    code = _code(k, "k")
-    if v.dtype is not k.dtype:
-        raise ValueError("k and v have one type")
-    kp, ks = _rows(k, "k", T, cache.n_kv_heads, cache.head_dim, dev)
-    vp, vs = _rows(v, "v", T, cache.n_kv_heads, cache.head_dim, dev)
-    table, n_seqs, width = _table(page_table, dev)
-    wp, wn = _workspace(ws, dev)
-    rc = _b.lib().moe_kv_write(cache.ref, kp, vp, code, ks, vs, T, None if seq is None else _int32(seq, "seq", (T,), dev),
-                               _int32(pos, "pos", (T,), dev), table, n_seqs, width, wp, wn, _raw_stream(dev))
+    T, dev, heads, dim = k.shape[0], cache.device, cache.n_kv_heads, cache.head_dim
+    code, shape = _CODES.get(k.dtype), (T, heads, dim)
+    if code is None or k.shape != shape or k.get_device() != dev:
+        raise _misfit("k", k, f"bf16 or fp32 {list(shape)}")
+    if v.dtype is not k.dtype or v.shape != shape or v.get_device() != dev:
+        raise _misfit("v", v, f"{k.dtype} {list(shape)}, as k")
+    pp, sp, table, n_seqs, width, wp, wn = _tokens(pos, seq, page_table, ws, T, dev)
+    rc = _b.lib().moe_kv_write(cache.ref, k.data_ptr(), v.data_ptr(), code, _row_stride(k, "k", heads, dim),
+                               _row_stride(v, "v", heads, dim), T, sp, pp, table, n_seqs, width, wp, wn, _raw_stream(dev))
     if rc:
         raise _b.MoeError(rc, "moe_kv_write")
 
@@ -149,16 +138,18 @@ def kv_read(cache: KVCache, pos: torch.Tensor, page_table: torch.Tensor, ws: tor
     [T, n_kv_heads, head_dim] of `dtype`, or of the given output tensors."""
     T, dev = pos.shape[0], cache.device
     shape = (T, cache.n_kv_heads, cache.head_dim)
-    k = k if k is not None else torch.empty(shape, dtype=dtype, device=cache.k.device)
-    v = v if v is not None else torch.empty(shape, dtype=k.dtype, device=cache.k.device)
-    code = _code(k, "k")
-    if v.dtype is not k.dtype:
-        raise ValueError("k and v have one type")
-    table, n_seqs, width = _table(page_table, dev)
-    wp, wn = _workspace(ws, dev)
-    rc = _b.lib().moe_kv_read(cache.ref, T, None if seq is None else _int32(seq, "seq", (T,), dev),
-                              _int32(pos, "pos", (T,), dev), table, n_seqs, width, _full(k, "k", shape, dev),
-                              _full(v, "v", shape, dev), code, wp, wn, _raw_stream(dev))
+    if k is None:
+        k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=cache.k.device)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=cache.k.device)
+    code = _CODES.get(k.dtype)
+    if code is None or k.shape != shape or k.get_device() != dev or not k.is_contiguous():
+        raise _misfit("k", k, f"bf16 or fp32 {list(shape)}, contiguous")
+    if v.dtype is not k.dtype or v.shape != shape or v.get_device() != dev or not v.is_contiguous():
+        raise _misfit("v", v, f"{k.dtype} {list(shape)}, contiguous")
+    pp, sp, table, n_seqs, width, wp, wn = _tokens(pos, seq, page_table, ws, T, dev)
+    rc = _b.lib().moe_kv_read(cache.ref, T, sp, pp, table, n_seqs, width, k.data_ptr(), v.data_ptr(), code, wp, wn,
+                              _raw_stream(dev))
     if rc:
         raise _b.MoeError(rc, "moe_kv_read")
     return k, v
@@ -171,25 +162,27 @@ def attn_decode(q: torch.Tensor, cache: KVCache, lens: torch.Tensor, page_table:
     fused projection's output) over the last `window` (0: all) of lens[b] cached tokens.  scale
     defaults to head_dim ** -0.5.  Returns out [B, n_heads, head_dim] bf16; lse [B, n_heads] fp32,
     where given, receives the log-sum-exp of the scores."""
-    if q.dim() != 3 or q.dtype is not torch.bfloat16:
-        raise ValueError("q is [sequences, n_heads, head_dim] bf16")
-    dev, dim = cache.device, cache.head_dim
-    B, H, _ = shape = q.shape
-    qp, qs = _rows(q, "q", B, H, dim, dev)
-    lp = _int32(lens, "lens", (B,), dev)
-    table, n_seqs, width = _table(page_table, dev)
+    dev, dim, shape = cache.device, cache.head_dim, q.shape
+    if q.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != dim or q.get_device() != dev:
+        raise _misfit("q", q, f"bf16 [sequences, n_heads, {dim}]")
+    B, H, _ = shape
+    if lens.dtype is not torch.int32 or lens.shape != (B,) or lens.get_device() != dev or not lens.is_contiguous():
+        raise _misfit("lens", lens, f"int32 [{B}], contiguous")
+    table, n_seqs, width, wp, wn = _table(page_table, ws, dev)
     if n_seqs != B:
-        raise ValueError("page_table holds one row a sequence")
+        raise _misfit("page_table", page_table, f"int32 [{B}, pages], a row a sequence")
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    elif out.dtype is not torch.bfloat16:
-        raise ValueError("out is bf16")
-    if lse is not None and lse.dtype is not torch.float32:
-        raise ValueError("lse is fp32")
-    wp, wn = _workspace(ws, dev)
-    rc = _b.lib().moe_attn_decode(cache.ref, qp, qs, H, B, lp, table, width, dim ** -0.5 if scale is None else scale,
-                                  window, _full(out, "out", shape, dev),
-                                  None if lse is None else _full(lse, "lse", (B, H), dev), wp, wn, _raw_stream(dev))
+    elif out.dtype is not torch.bfloat16 or out.shape != shape or out.get_device() != dev or not out.is_contiguous():
+        raise _misfit("out", out, f"bf16 {list(shape)}, contiguous")
+    lp = None
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (B, H) or lse.get_device() != dev or not lse.is_contiguous():
+            raise _misfit("lse", lse, f"fp32 [{B}, {H}], contiguous")
+        lp = lse.data_ptr()
+    rc = _b.lib().moe_attn_decode(cache.ref, q.data_ptr(), _row_stride(q, "q", H, dim), H, B, lens.data_ptr(), table, width,
+                                  dim ** -0.5 if scale is None else scale, window, out.data_ptr(), lp, wp, wn,
+                                  _raw_stream(dev))
     if rc:
         raise _b.MoeError(rc, "moe_attn_decode")
     return out
@@ -203,41 +196,47 @@ def block_norm(residual: torch.Tensor, w_pre: Optional[torch.Tensor], y: Optiona
     y None: the norm of the residual alone; w_post or gate None: without them; gate [d] (for all
     tokens) or [T, d]; w_pre None: the residual sum alone.  Returns (residual_out, x): residual_out
     defaults to `residual`, updated in place."""
-    if residual.dim() != 2:
-        raise ValueError("residual is [tokens, d]")
-    T, d = shape = residual.shape
-    dev = residual.get_device()
-    if dev < 0:
-        raise ValueError("libmoe takes CUDA tensors")
-    code = _code(residual, "residual")
-    rp = _full(residual, "residual", shape, dev)
+    shape, dev, code = residual.shape, residual.get_device(), _CODES.get(residual.dtype)
+    if dev < 0 or code is None or len(shape) != 2 or not residual.is_contiguous():
+        raise _misfit("residual", residual, "bf16 or fp32 [tokens, d], contiguous and on a GPU")
+    T, d = shape
+    rp = residual.data_ptr()
     yp, y_code, post, pre, gp, gs, g_code, xp, x_code = None, 0, None, None, None, 0, 0, None, 0
     if y is not None:
-        yp, y_code = _full(y, "y", shape, dev), _code(y, "y")
+        y_code = _CODES.get(y.dtype)
+        if y_code is None or y.shape != shape or y.get_device() != dev or not y.is_contiguous():
+            raise _misfit("y", y, f"bf16 or fp32 {list(shape)}, contiguous")
+        yp = y.data_ptr()
     if w_post is not None:
-        post = _full(w_post, "w_post", (d,), dev)
-        if w_post.dtype is not torch.float32:
-            raise ValueError("w_post is fp32")
+        if (w_post.dtype is not torch.float32 or w_post.shape != (d,) or w_post.get_device() != dev
+                or not w_post.is_contiguous()):
+            raise _misfit("w_post", w_post, f"fp32 [{d}], contiguous")
+        post = w_post.data_ptr()
     if gate is not None:
-        per_token = gate.dim() == 2
-        if gate.shape != (shape if per_token else (d,)) or gate.get_device() != dev or (gate.stride(-1) != 1 and d > 1):
-            raise ValueError("gate is [d] or [tokens, d], its rows contiguous and on the same GPU")
-        gp, g_code = gate.data_ptr(), _code(gate, "gate")
+        g_code, per_token = _CODES.get(gate.dtype), gate.dim() == 2
+        if (g_code is None or gate.shape != (shape if per_token else (d,)) or gate.get_device() != dev
+                or (gate.stride(-1) != 1 and d > 1)):
+            raise _misfit("gate", gate, f"bf16 or fp32 [{d}] or {list(shape)} with contiguous rows")
+        gp = gate.data_ptr()
         gs = gate.stride(0) if per_token and T > 1 else 0
     if residual_out is None:
         residual_out = residual
         op = None if y is None else rp  # without y the residual stays as it is
     else:
-        op = _full(residual_out, "residual_out", shape, dev)
-        if residual_out.dtype is not residual.dtype:
-            raise ValueError("residual_out has the residual's type")
+        if (residual_out.dtype is not residual.dtype or residual_out.shape != shape or residual_out.get_device() != dev
+                or not residual_out.is_contiguous()):
+            raise _misfit("residual_out", residual_out, f"{residual.dtype} {list(shape)}, contiguous, as the residual")
+        op = residual_out.data_ptr()
     if w_pre is not None:
-        pre = _full(w_pre, "w_pre", (d,), dev)
-        if w_pre.dtype is not torch.float32:
-            raise ValueError("w_pre is fp32")
+        if w_pre.dtype is not torch.float32 or w_pre.shape != (d,) or w_pre.get_device() != dev or not w_pre.is_contiguous():
+            raise _misfit("w_pre", w_pre, f"fp32 [{d}], contiguous")
+        pre = w_pre.data_ptr()
         if out is None:
             out = torch.empty(shape, dtype=x_dtype, device=residual.device)
-        xp, x_code = _full(out, "out", shape, dev), _code(out, "out")
+        x_code = _CODES.get(out.dtype)
+        if x_code is None or out.shape != shape or out.get_device() != dev or not out.is_contiguous():
+            raise _misfit("out", out, f"bf16 or fp32 {list(shape)}, contiguous")
+        xp = out.data_ptr()
     elif out is not None:
         raise ValueError("an output norm needs w_pre")
     rc = _b.lib().moe_block_norm(yp, y_code, post, gp, g_code, gs, alpha, rp, op, code, pre, xp, x_code, T, d, eps,
