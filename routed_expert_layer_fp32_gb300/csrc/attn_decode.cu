@@ -237,7 +237,7 @@ struct Walk {
     b = b0;
     if (pos >= hi) return;
     span = span_of<S>(a, b);
-    seg = off0 / span.tiles;
+    seg = unsigned(off0) / unsigned(span.tiles);
     tile = off0 - seg * span.tiles;
     take = min(span.tiles - tile, hi - pos);
   }
@@ -253,6 +253,9 @@ struct Walk {
     }
     take = min(span.tiles, hi - pos);
   }
+  __device__ __forceinline__ int kv(int head_blocks) const {  // the segment's kv head
+    return head_blocks == 1 ? seg : unsigned(seg) / unsigned(head_blocks);
+  }
   __device__ __forceinline__ bool whole() const { return take == span.tiles; }  // the segment is all ours
 };
 
@@ -260,13 +263,13 @@ struct Walk {
 struct Parts {
   int each, more;
   __device__ __forceinline__ Parts(int total, int ctas) {
-    each = ctas > 0 ? total / ctas : 0;
+    each = ctas > 0 ? unsigned(total) / unsigned(ctas) : 0;
     more = total - each * ctas;
   }
   __device__ __forceinline__ int begin(int cta) const { return cta * each + min(cta, more); }
   __device__ __forceinline__ int owner(int tile) const {
     const int wide = more * (each + 1);
-    return tile < wide ? tile / (each + 1) : more + (tile - wide) / each;
+    return tile < wide ? unsigned(tile) / unsigned(each + 1) : more + unsigned(tile - wide) / unsigned(each);
   }
 };
 
@@ -897,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // --------------------------------------------------------------- producers ------------
       bool ok = true;
       for (; ok && !walk.done(); walk.next(a, segs)) {
-        const int kv = walk.seg / head_blocks;
+        const int kv = walk.kv(head_blocks);
         const int t_begin = walk.span.tile0 + walk.tile;
         const int32_t* pages = a.table.pages + int64_t(walk.b) * a.table.max_pages;
         // The pages of 32 boxes at a time, a lane each, and of the next 32 ahead of their use; with the
@@ -966,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kQueryWarp) {
       // ---------------------------------------------------------------- queries -------------
       for (; !walk.done(); walk.next(a, segs), ++seg) {
-        const int kv = walk.seg / head_blocks, hb = walk.seg % head_blocks, slot = seg % S::kSlots;
+        const int kv = walk.kv(head_blocks), hb = walk.seg - kv * head_blocks, slot = seg % S::kSlots;
         if (!__all_sync(0xffffffffu, wait_part(&ctl->q_empty[slot], ((seg / S::kSlots) & 1) ^ 1, &ctl->abort))) {
           if (lane == 0) report_timeout_flag(a.table.status_flags, 41);
           break;
@@ -1001,7 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int joins = 0;  // passes through the join buffer so far
     Compute mine_w(row0, lane, box);
     for (; !walk.done(); walk.next(a, segs), ++seg) {
-      const int hb = walk.seg % head_blocks, slot = seg % S::kSlots;
+      const int hb = walk.seg - walk.kv(head_blocks) * head_blocks, slot = seg % S::kSlots;
       if (!wait(&ctl->q_full[slot], (seg / S::kSlots) & 1, &ctl->abort)) timed_out = true;
       mine_w.begin(queries + slot * S::kQueries, lane);
       __syncwarp();
@@ -1049,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int joins = 0, n_joints = 0;
   Joint joints[2] = {};
   for (; !walk.done(); walk.next(a, segs)) {
-    const int kv = walk.seg / head_blocks, hb = walk.seg % head_blocks;
+    const int kv = walk.kv(head_blocks), hb = walk.seg - kv * head_blocks;
     const int heads = min(S::kHeads, group - hb * S::kHeads);
     const int64_t row = int64_t(walk.b) * a.n_heads + kv * group + hb * S::kHeads;  // of the first head in out
     const bool whole = walk.whole();  // finished here, or a partial result
