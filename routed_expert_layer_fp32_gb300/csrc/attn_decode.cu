@@ -21,14 +21,23 @@
 // back to 0 afterwards) joins them in CTA order, so the result does not depend on timing.
 //
 // In a CTA, two warps are producers: they look up pages and start the tiles' TMA copies into a ring of
-// shared-memory stages.  Another lays the next segments' queries out as operands.  Eight warps
+// shared-memory stages.  Two more lay the next segments' queries out as operands.  Eight warps
 // compute, in groups that take the tiles in turn; a warp has kPerWarp tokens of each of its group's
 // tiles and its own m, sum and accumulator, and at a segment's end leaves them in shared memory and
-// goes on.  Four warps add the eight results up, write the output or the partial result, and join
-// partial results.  So neither the copies nor the products wait for a segment's end (with all of that
-// in the eight warps, 128 windows of 513 tokens took 31.4 us, like this 22.7).  A stage belongs to one
-// group: a barrier's wait tells only the parity of the phase, so whoever waits for a stage has to have
-// seen each of its phases.
+// goes on.  Four warps add up the results of the groups that had a tile of the segment, write the
+// output or the partial result, and join partial results.  So neither the copies nor the products
+// wait for a segment's end (with all of that in the eight warps, 128 windows of 513 tokens took
+// 31.4 us, like this 21.3).  A group passes over segments without a tile of its own, so that several
+// short ones are worked on at once, each group with a join buffer of its own (177 sequences of up to
+// 42 tokens, 8 kv heads of 8 query heads, 192 wide, E4M3: with all eight warps at every segment's
+// end and one warp for the queries 79 us, like this 43).  A stage, and a join buffer, belongs to one
+// group: a barrier's wait tells only the parity of the phase, so whoever waits for it has to have seen
+// each of its phases.
+//
+// Code is short where it can be: sixteen warps run six programs, and where segments are short the
+// instruction cache does not hold them.  So a tile's whole and its masked rows go one way (two copies of
+// the product code, one without masks, gained 1 % on long rows, and cost 68 us against 43 there, and
+// 88 against 62 for 52 mixed lengths of up to 499 tokens, groups of 12, 256 wide).
 //
 // Starting a copy holds a warp up for 100 to 200 cycles, enough to fall behind the memory with the 2 KB
 // copies of 16-token pages if it computes anything else there: there is no division a tile, each lane
@@ -55,6 +64,7 @@ namespace {
 constexpr int kWarps = 8;      // compute
 constexpr int kProducers = 2;  // start copies
 constexpr int kQueryWarp = kWarps + kProducers;
+constexpr int kQueryWarps = 2;  // the second also zeroes the rows of empty sequences
 constexpr int kEndWarp = kWarps + 4;  // the first of those that end segments
 constexpr int kEndThreads = 128;
 constexpr int kThreads = kEndWarp * 32 + kEndThreads;
@@ -100,7 +110,8 @@ struct Shape {
   static constexpr int kSlot = kHeads * (kDim + 2);          // floats of a partial result
   static constexpr int kMaxStages = 16;
   struct Control {
-    uint64_t full[kMaxStages], empty[kMaxStages], q_full[kSlots], q_empty[kSlots], join_full, join_empty, merge_full;
+    uint64_t full[kMaxStages], empty[kMaxStages], q_full[kSlots], q_empty[kSlots];
+    uint64_t join_full[kGroups], join_empty[kGroups], merge_full;
     uint32_t valid[kMaxStages];  // a bit for each 16 tokens of the tile: copied
     int abort;
     int b0, off0, last, scan[kThreads / 32];
@@ -213,22 +224,29 @@ struct Span {  // the tokens of one sequence that are seen, and their tiles
 };
 
 template <typename S>
-__device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
+__device__ __forceinline__ Span span_of_len(const AttnArgs& a, int len) {
   const int room = a.table.max_pages * a.cache.page;
   Span s;
-  s.end = max(0, min(__ldg(a.lens + b), room));
+  s.end = max(0, min(len, room));
   s.first = a.window > 0 ? max(0, s.end - a.window) : 0;
   s.tile0 = s.first / S::kTokens;
   s.tiles = (s.end + S::kTokens - 1) / S::kTokens - s.tile0;
   return s;
 }
 
-// Walks a CTA's part of the line, segment by segment.
+template <typename S>
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
+  return span_of_len<S>(a, __ldg(a.lens + b));
+}
+
+// Walks a CTA's part of the line, segment by segment.  The length of the sequence to come is read one
+// sequence ahead: where they are short, a trip to memory would be most of a segment's time.
 template <typename S>
 struct Walk {
   int b, seg, tile;  // sequence, segment in it, first tile (of the segment's) that is ours
   int take;          // how many tiles are ours
   int pos, hi;       // on the line (below 2^31 tiles)
+  int len_to_come;   // of sequence b + 1
   Span span;
 
   __device__ __forceinline__ void start(const AttnArgs& a, int b0, int off0, int lo, int hi_) {
@@ -236,6 +254,7 @@ struct Walk {
     hi = hi_;
     b = b0;
     if (pos >= hi) return;
+    len_to_come = __ldg(a.lens + min(b + 1, a.B - 1));
     span = span_of<S>(a, b);
     seg = unsigned(off0) / unsigned(span.tiles);
     tile = off0 - seg * span.tiles;
@@ -248,8 +267,10 @@ struct Walk {
     if (pos >= hi) return;
     if (++seg == segs) {
       seg = 0;
-      do span = span_of<S>(a, ++b);
-      while (span.tiles == 0);  // pos < hi: a sequence with tiles follows
+      do {
+        span = span_of_len<S>(a, len_to_come);
+        len_to_come = __ldg(a.lens + min(++b + 1, a.B - 1));
+      } while (span.tiles == 0);  // pos < hi: a sequence with tiles follows
     }
     take = min(span.tiles, hi - pos);
   }
@@ -279,16 +300,7 @@ struct Parts {
 struct TileView {
   uint32_t k, v;        // shared-memory addresses of the key and value tiles
   const uint8_t* exps;  // of the keys; the values' follow kTokens further
-  int pos0;             // position of the warp's first token
-  int first, end;       // the positions that are seen
-  uint32_t valid;       // a bit for each 16 of the warp's tokens: copied
-  __device__ __forceinline__ bool seen(int r) const {
-    return (valid >> (r / 16) & 1) && pos0 + r >= first && pos0 + r < end;
-  }
-  // 0xffff a seen token: tokens r (low half) and r + 1
-  __device__ __forceinline__ uint32_t keep2(int r) const {
-    return (seen(r) ? 0xffffu : 0u) | (seen(r + 1) ? 0xffff0000u : 0u);
-  }
+  uint32_t seen;        // a bit for each of the warp's tokens
 };
 
 // Addresses for ldmatrix.  A tile lies in shared memory box by box (the tokens of one copy, a multiple
@@ -313,6 +325,23 @@ struct Rows {
     return tile + at[block] + i / kPairs * span + (uint32_t((i % kPairs) << 5) ^ flip);
   }
 };
+
+// Zeros in the rows of a tile of values that a warp (rows row0 .. row0 + kPerWarp - 1) does not see: what
+// lies there may be no number, and a weight of 0 would not make it vanish.  Lanes take rows, and chunks
+// in an order of their own against bank conflicts.
+template <typename S>
+__device__ __forceinline__ void clear_rows(uint32_t tile, int row0, int box, uint32_t seen, int lane) {
+  constexpr int kLanes = 32 / S::kPerWarp;  // of a row
+  const int i = lane % S::kPerWarp, r = row0 + i;
+  if (seen >> i & 1) return;
+  const uint32_t at = tile + uint32_t(r / box * box * S::kRow + r % box * S::kSpan);
+  constexpr int kChunks = S::kSpan / 16;  // of a span
+#pragma unroll 4
+  for (int c = lane / S::kPerWarp; c < S::kRow / 16; c += kLanes) {
+    const uint32_t chunk = at + c / kChunks * (box * S::kSpan) + (((c ^ r) & (kChunks - 1)) << 4);
+    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(chunk), "r"(0) : "memory");
+  }
+}
 
 // One warp's running result over a bf16 cache.  Scores: keys (16 tokens x 16 elements, as they lie)
 // times queries; the weights, rounded to bf16 (the type of the values: a product's operands have
@@ -375,8 +404,8 @@ struct WarpBf16 {
     }
   }
 
-  template <bool kWhole>  // all of the warp's tokens are seen
   __device__ __forceinline__ void tile(const TileView& tv) {
+    const uint32_t seen = tv.seen >> g;
     float s[kMT][kNB][4];
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
@@ -397,7 +426,7 @@ struct WarpBf16 {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float x = (s[mt][nb][i] + s2[nb][i]) * factor;
-          s[mt][nb][i] = kWhole || tv.seen(mt * 16 + (i >> 1) * 8 + g) ? x : -INFINITY;
+          s[mt][nb][i] = seen >> (mt * 16 + (i >> 1) * 8) & 1 ? x : -INFINITY;
         }
     }
     float base[kNB][2], fix[kNB][2];
@@ -441,13 +470,10 @@ struct WarpBf16 {
         }
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
-      // what lies in rows that are not seen may be no number: 0 there
-      const uint32_t keep0 = kWhole ? 0u : tv.keep2(mt * 16 + 2 * t), keep1 = kWhole ? 0u : tv.keep2(mt * 16 + 8 + 2 * t);
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         uint32_t r[4];
         ldmatrix4_trans(v_rows(tv.v, mt, ks), r);
-        if (!kWhole) r[0] &= keep0, r[1] &= keep0, r[2] &= keep1, r[3] &= keep1;
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) mma_bf16_16x8x16(acc[ks][nb], r, w[mt][nb][0], w[mt][nb][1]);
       }
@@ -515,52 +541,52 @@ struct WarpE4M3 {
   __device__ __forceinline__ WarpE4M3(int row0, int lane, int box)
       : rows(row0 + (lane & 15), lane >> 4, box), g(lane >> 2), t(lane & 3) {}
 
-  // hi or lo codes of four query elements
-  static __device__ __forceinline__ uint32_t split4(uint2 u, float down, bool lo) {
+  // The hi (x) and lo (y) codes of four query elements.
+  static __device__ __forceinline__ uint2 split4(uint2 u, float down) {
     const float x0 = __uint_as_float(u.x << 16) * down, x1 = __uint_as_float(u.x & 0xffff0000u) * down;
     const float x2 = __uint_as_float(u.y << 16) * down, x3 = __uint_as_float(u.y & 0xffff0000u) * down;
     const uint32_t h01 = e4m3_code2(x0, x1), h23 = e4m3_code2(x2, x3);
     const float2 f01 = float2_of_codes(h01), f23 = float2_of_codes(h23);
     const uint32_t l01 = e4m3_code2((x0 - f01.x) * 32.0f, (x1 - f01.y) * 32.0f);
     const uint32_t l23 = e4m3_code2((x2 - f23.x) * 32.0f, (x3 - f23.y) * 32.0f);
-    return lo ? l01 | l23 << 16 : h01 | h23 << 16;
+    return make_uint2(h01 | h23 << 16, l01 | l23 << 16);
   }
 
   // Register [ks][nb][i] of lane (g, t): column g of block nb (head nb * 4 + g / 2, its hi or lo),
-  // elements 32 ks + 16 i + 4t and the three after.
+  // elements 32 ks + 16 i + 4t and the three after.  The two lanes of a head split the elements of an i
+  // each and exchange.
   static __device__ __forceinline__ void lay_out(uint8_t* queries, const __nv_bfloat16* q, int heads, int dim,
                                                  float scale_log2e, int lane) {
-    const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2, t = lane & 3, odd = g & 1;
 #pragma unroll 1
     for (int nb = 0; nb < kNB; ++nb) {
       const int h = nb * 4 + (g >> 1);
-      const uint2* row = reinterpret_cast<const uint2*>(q + int64_t(h) * dim) + t;
-      uint2 u[kKS][2];
+      const uint2* row = reinterpret_cast<const uint2*>(q + int64_t(h) * dim) + t + odd * 4;
+      uint2 u[kKS];
       float top = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks)
+        u[ks] = h < heads && ks * 32 + odd * 16 < dim ? __ldg(row + ks * 8) : make_uint2(0u, 0u);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          u[ks][i] = h < heads && ks * 32 + i * 16 < dim ? __ldg(row + ks * 8 + i * 4) : make_uint2(0u, 0u);
+      for (int ks = 0; ks < kKS; ++ks) {
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[ks].x << 16)), fabsf(__uint_as_float(u[ks].x & 0xffff0000u))));
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[ks].y << 16)), fabsf(__uint_as_float(u[ks].y & 0xffff0000u))));
+      }
 #pragma unroll
-      for (int ks = 0; ks < kKS; ++ks)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[ks][i].x << 16)), fabsf(__uint_as_float(u[ks][i].x & 0xffff0000u))));
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[ks][i].y << 16)), fabsf(__uint_as_float(u[ks][i].y & 0xffff0000u))));
-        }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       // times 2^-e the largest is in [2^7, 2^8)
       const int e = min(120, max(-100, int(__float_as_uint(top) >> 23) - 127 - 7));
       const float down = __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll
-      for (int ks = 0; ks < kKS; ++ks)
+      for (int ks = 0; ks < kKS; ++ks) {
+        const uint2 mine = split4(u[ks], down);
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? mine.x : mine.y, 4);
         *reinterpret_cast<uint2*>(queries + ((nb * kKS + ks) * 32 + lane) * 8) =
-            make_uint2(split4(u[ks][0], down, g & 1), split4(u[ks][1], down, g & 1));
+            odd ? make_uint2(other, mine.y) : make_uint2(mine.x, other);
+      }
       // a query with an infinity or NaN has no finite scores
       const float lost = top < INFINITY ? 1.0f : __uint_as_float(0x7fc00000u);
-      if (t == 0 && !(g & 1))
+      if (t == 0 && !odd)
         reinterpret_cast<float*>(queries + S::kQueryRegs * 128)[h] =
             scale_log2e * (__uint_as_float(uint32_t(127 + e) << 23) * lost);
     }
@@ -582,8 +608,8 @@ struct WarpE4M3 {
     }
   }
 
-  template <bool kWhole>
   __device__ __forceinline__ void tile(const TileView& tv) {
+    const uint32_t seen_bits = tv.seen >> g;
     float s[2][kNB][2];  // tokens g and g + 8 of both blocks, head t of each column block
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
@@ -614,7 +640,7 @@ struct WarpE4M3 {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int r = mt * 16 + half * 8 + g;
-        const bool seen = kWhole || tv.seen(r);
+        const bool seen = seen_bits >> (mt * 16 + half * 8) & 1;
         const float k_unit = exp_value(tv.exps[r]);
         const uint32_t ve = tv.exps[S::kTokens + r];
         const float c = float(max(int(ve) - kExpBias, kMinExp));
@@ -664,18 +690,12 @@ struct WarpE4M3 {
       sum[nb] = fmaf(all, f, sum[nb]);
       into[nb] = f * (1.0f / 256.0f);
     }
-    uint32_t keep[2][2];
-    if (!kWhole) {
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) keep[mt][0] = tv.keep2(mt * 16 + 2 * t), keep[mt][1] = tv.keep2(mt * 16 + 8 + 2 * t);
-    }
 #pragma unroll
     for (int i = 0; i < kKS; ++i) {
       uint32_t r[2][4];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         ldmatrix4_trans(rows(tv.v, mt, i), r[mt]);
-        if (!kWhole) r[mt][0] &= keep[mt][0], r[mt][1] &= keep[mt][1], r[mt][2] &= keep[mt][0], r[mt][3] &= keep[mt][1];
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -827,8 +847,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->q_full[i], 1);
       mbar_init(&ctl->q_empty[i], kWarps);
     }
-    mbar_init(&ctl->join_full, kWarps);
-    mbar_init(&ctl->join_empty, kEndThreads / 32);
+    for (int i = 0; i < S::kGroups; ++i) {
+      mbar_init(&ctl->join_full[i], S::kGroupWarps);
+      mbar_init(&ctl->join_empty[i], kEndThreads / 32);
+    }
     mbar_init(&ctl->merge_full, 1);
     ctl->abort = 0;
     mbar_fence_init();
@@ -887,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
 
   // Every warp walks the CTA's part by itself; `it` counts its tiles (the ring's position), `seg` its
-  // segments.  Only the producers' and the query warp's walks end early, at a wait that ran out: the
+  // segments.  Only the producers' and the query warps' walks end early, at a wait that ran out: the
   // others go on through the same barriers on whatever they find, and the status record says that it
   // is no result.
   Walk<S> walk;
@@ -957,18 +979,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok && lane == 0) {
-        // a wait ran out: this CTA's copies must land before it ends (bounded again)
-        report_timeout_flag(a.table.status_flags, 40);
+      if (lane == 0) {
+        if (!ok) report_timeout_flag(a.table.status_flags, 40);
+        // this CTA's copies must land before it ends, whatever became of those who wait for them
         const unsigned long long t0 = global_timer_ns();
         for (int i = max(0, it - S::kStages); i < it; ++i)
           while (!mbar_try_wait(&ctl->full[i % S::kStages], (i / S::kStages) & 1) &&
                  global_timer_ns() - t0 < kWaitLimitNs) {
           }
       }
-    } else if (warp == kQueryWarp) {
-      // ---------------------------------------------------------------- queries -------------
+    } else {
+      if (warp == kQueryWarp + 1) {
+        // ----------------------------------------- sequences without a token: zeros ---------
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+          if (span_of<S>(a, b).tiles != 0) continue;
+          const int n = a.n_heads * c.dim / 8;
+          uint4* out = reinterpret_cast<uint4*>(a.out + int64_t(b) * a.n_heads * c.dim);
+          for (int i = lane; i < n; i += 32) out[i] = make_uint4(0, 0, 0, 0);
+          if (a.lse)
+            for (int h = lane; h < a.n_heads; h += 32) a.lse[int64_t(b) * a.n_heads + h] = -INFINITY;
+        }
+      }
+      // ------------------------------- queries, the segments in turn by the two warps -------
       for (; !walk.done(); walk.next(a, segs), ++seg) {
+        if (seg % kQueryWarps != warp - kQueryWarp) continue;
         const int kv = walk.kv(head_blocks), hb = walk.seg - kv * head_blocks, slot = seg % S::kSlots;
         if (!__all_sync(0xffffffffu, wait_part(&ctl->q_empty[slot], ((seg / S::kSlots) & 1) ^ 1, &ctl->abort))) {
           if (lane == 0) report_timeout_flag(a.table.status_flags, 41);
@@ -980,18 +1014,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->q_full[slot]);
       }
-    } else {
-      // ------------------------------------------- sequences without a token: zeros ---------
-      for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        if (span_of<S>(a, b).tiles != 0) continue;
-        const int n = a.n_heads * c.dim / 8;
-        uint4* out = reinterpret_cast<uint4*>(a.out + int64_t(b) * a.n_heads * c.dim);
-        if (warp == kQueryWarp + 1) {
-          for (int i = lane; i < n; i += 32) out[i] = make_uint4(0, 0, 0, 0);
-          if (a.lse)
-            for (int h = lane; h < a.n_heads; h += 32) a.lse[int64_t(b) * a.n_heads + h] = -INFINITY;
-        }
-      }
     }
     return;
   }
@@ -1001,31 +1023,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     more_registers<kComputeRegs>();
     const int wg = warp / S::kGroupWarps, row0 = (warp % S::kGroupWarps) * S::kPerWarp;
     bool timed_out = false;
-    int joins = 0;  // passes through the join buffer so far
+    int joins = 0;  // the group's passes through the join buffer so far
     Compute mine_w(row0, lane, box);
-    for (; !walk.done(); walk.next(a, segs), ++seg) {
+    for (; !walk.done(); it += walk.take, walk.next(a, segs), ++seg) {
       const int hb = walk.seg - walk.kv(head_blocks) * head_blocks, slot = seg % S::kSlots;
+      const int n0 = unsigned(wg - it) % S::kGroups;  // the group's first tile of the segment
       if (!wait(&ctl->q_full[slot], (seg / S::kSlots) & 1, &ctl->abort)) timed_out = true;
+      // (under a condition, n0 < walk.take, more registers spill: 16 heads, 64 x 8k bf16 68.1 us against 66.5)
       mine_w.begin(queries + slot * S::kQueries, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->q_empty[slot]);
+      if (n0 >= walk.take) continue;
       TileView tv;
-      tv.first = walk.span.first;
-      tv.end = walk.span.end;
-      for (int n = 0; n < walk.take; ++n, ++it) {
-        const int stage = it % S::kStages;
-        if (stage % S::kGroups != wg) continue;
-        if (!wait(&ctl->full[stage], (it / S::kStages) & 1, &ctl->abort)) timed_out = true;
+      for (int n = n0; n < walk.take; n += S::kGroups) {
+        const int stage = (it + n) % S::kStages;
+        if (!wait(&ctl->full[stage], ((it + n) / S::kStages) & 1, &ctl->abort)) timed_out = true;
         tv.k = smem_u32(smem + size_t(stage) * S::kStage);
         tv.v = tv.k + S::kTile;
         tv.exps = exps + stage * S::kExps + row0;
-        tv.pos0 = (walk.span.tile0 + walk.tile + n) * S::kTokens + row0;
-        constexpr uint32_t kAll = (1u << (S::kPerWarp / 16)) - 1u;
-        tv.valid = ctl->valid[stage] >> (row0 / 16) & kAll;
-        if (tv.valid == kAll && tv.pos0 >= tv.first && tv.pos0 + S::kPerWarp <= tv.end)
-          mine_w.template tile<true>(tv);
-        else if (tv.valid != 0 && tv.pos0 < tv.end && tv.pos0 + S::kPerWarp > tv.first)
-          mine_w.template tile<false>(tv);
+        // the warp's tokens [from, to) of the tile lie in what is seen
+        const int pos0 = (walk.span.tile0 + walk.tile + n) * S::kTokens + row0;
+        const int from = max(0, walk.span.first - pos0), to = min(S::kPerWarp, walk.span.end - pos0);
+        constexpr uint32_t kAll = 0xffffffffu >> (32 - S::kPerWarp);
+        tv.seen = from < to ? kAll >> (S::kPerWarp - to + from) << from : 0u;
+        const uint32_t copied = ctl->valid[stage] >> (row0 / 16);
+        if (!(copied & 1)) tv.seen &= ~0xffffu;
+        if (S::kPerWarp == 32 && !(copied & 2)) tv.seen &= 0xffffu;
+        if (tv.seen != 0) {
+          if (tv.seen != kAll) {
+            clear_rows<S>(tv.v, row0, box, tv.seen, lane);
+            fence_proxy_async_smem();  // before the next copy into these rows
+            __syncwarp();
+          }
+          mine_w.tile(tv);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->empty[stage]);
       }
@@ -1033,11 +1064,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for_constants(std::make_integer_sequence<int, S::kPasses>{}, [&](auto pass) {
         constexpr int kPass = decltype(pass)::value;
         if (kPass * S::kPassDim >= c.dim) return;
-        if (!wait(&ctl->join_empty, (joins & 1) ^ 1, &ctl->abort)) timed_out = true;
+        if (!wait(&ctl->join_empty[wg], (joins & 1) ^ 1, &ctl->abort)) timed_out = true;
         if (kPass == 0) mine_w.publish_sums(ctl->m[warp], ctl->sum[warp]);
         mine_w.template publish<kPass>(join + warp * S::kJoinWarp, heads);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->join_full);
+        if (lane == 0) mbar_arrive(&ctl->join_full[wg]);
         ++joins;
       });
     }
@@ -1049,9 +1080,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   fewer_registers<kEndRegs>();
   const int tid = threadIdx.x - kEndWarp * 32;
   bool timed_out = false;
-  int joins = 0, n_joints = 0;
+  int n_joints = 0;
+  uint32_t phases = 0;  // a bit for each group: the parity of its next pass through the join buffer
   Joint joints[2] = {};
-  for (; !walk.done(); walk.next(a, segs)) {
+  for (; !walk.done(); it += walk.take, walk.next(a, segs)) {
     const int kv = walk.kv(head_blocks), hb = walk.seg - kv * head_blocks;
     const int heads = min(S::kHeads, group - hb * S::kHeads);
     const int64_t row = int64_t(walk.b) * a.n_heads + kv * group + hb * S::kHeads;  // of the first head in out
@@ -1060,19 +1092,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // slot 0: a segment that began before this CTA's part; slot 1: one that begins in it
     float* slot = slots + (size_t(blockIdx.x) * 2 + (walk.tile == 0)) * S::kSlot;
 
-    // -------- the warps' results --------
-    for (int d0 = 0; d0 < c.dim; d0 += S::kPassDim, ++joins) {
-      if (!wait_part(&ctl->join_full, joins & 1, &ctl->abort)) timed_out = true;
+    // -------- the results of the warps that had a tile of it --------
+    uint32_t groups = 0;
+#pragma unroll
+    for (int i = 0; i < S::kGroups; ++i) groups |= uint32_t(i < walk.take) << unsigned(it + i) % S::kGroups;
+    for (int d0 = 0; d0 < c.dim; d0 += S::kPassDim, phases ^= groups) {
+#pragma unroll
+      for (int i = 0; i < S::kGroups; ++i)
+        if ((groups >> i & 1) && !wait_part(&ctl->join_full[i], phases >> i & 1, &ctl->abort)) timed_out = true;
       constexpr int kVecs = S::kPassDim / 4;
-      for (int i = tid; i < heads * kVecs; i += kEndThreads) {
-        const int h = i / kVecs, d = (i % kVecs) * 4;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ctl->m[w][h]);
-        const float base = top == -INFINITY ? 0.0f : top;
-        float all = 0.0f, v[4] = {};
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+      for (int item = tid; item < heads * kVecs; item += kEndThreads) {
+        const int h = item / kVecs, d = (item % kVecs) * 4;
+        float top = -INFINITY, all = 0.0f, v[4] = {};
+        auto top_of = [&](int w) { top = fmaxf(top, ctl->m[w][h]); };
+        auto add = [&](int w, float base) {
           const float f = exp2_fast(ctl->m[w][h] - base);
           const float4 x = *reinterpret_cast<const float4*>(join + w * S::kJoinWarp + h * S::kJoinRow + d);
           all = fmaf(ctl->sum[w][h], f, all);
@@ -1080,13 +1113,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           v[1] = fmaf(x.y, f, v[1]);
           v[2] = fmaf(x.z, f, v[2]);
           v[3] = fmaf(x.w, f, v[3]);
+        };
+        if (groups == (1u << S::kGroups) - 1) {
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) top_of(w);
+          const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) add(w, base);
+        } else {
+          for (uint32_t left = groups; left; left &= left - 1)
+#pragma unroll
+            for (int k = 0; k < S::kGroupWarps; ++k) top_of((__ffs(left) - 1) * S::kGroupWarps + k);
+          const float base = top == -INFINITY ? 0.0f : top;
+          for (uint32_t left = groups; left; left &= left - 1)
+#pragma unroll
+            for (int k = 0; k < S::kGroupWarps; ++k) add((__ffs(left) - 1) * S::kGroupWarps + k, base);
         }
         if (whole) {
           const float scale = all == 0.0f ? 0.0f : 1.0f / all;
           if (d0 + d < c.dim)
             *reinterpret_cast<uint2*>(a.out + (row + h) * c.dim + d0 + d) =
                 make_uint2(pack_bf16x2(v[0] * scale, v[1] * scale), pack_bf16x2(v[2] * scale, v[3] * scale));
-          if (d0 == 0 && d == 0 && a.lse) a.lse[row + h] = all == 0.0f ? -INFINITY : base * kLn2 + logf(all);
+          if (d0 == 0 && d == 0 && a.lse) a.lse[row + h] = all == 0.0f ? -INFINITY : top * kLn2 + logf(all);
         } else {
           if (d0 + d < c.dim)
             __stcg(reinterpret_cast<float4*>(slot + 2 * S::kHeads + h * S::kDim + d0 + d),
@@ -1098,7 +1146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->join_empty);
+      if (lane < S::kGroups && (groups >> lane & 1)) mbar_arrive(&ctl->join_empty[lane]);
     }
     if (whole) continue;
 
