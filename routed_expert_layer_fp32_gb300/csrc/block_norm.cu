@@ -28,6 +28,8 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return s;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Eight elements as they lie in memory.
 template <typename T>
 struct Raw8 {
@@ -81,17 +83,31 @@ __global__ void __launch_bounds__(kResident, 1) k_block_norm(NormArgs a) {
       if (y) y_next[j].load(y + at);
     }
   };
-  fetch(blockIdx.x);
+  // The next row's registers are for those that have them: two groups of fp32 would spill, and have the
+  // next row brought to L2 instead (732 rows of 16384, fp32 y: 29.9 us against 32.3).
+  constexpr bool kAhead = kVecs == 1 || sizeof(Y) + sizeof(R) == 4;
+  if (kAhead) fetch(blockIdx.x);
   int turn = 0;
   for (int row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 2) {
     const int64_t row0 = int64_t(row) * a.d;
+    const int next = row + gridDim.x;
     float r[kVecs][8], z[kVecs][8];
+    if (!kAhead) fetch(row);
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       r_next[j].unpack(r[j]);
       y_next[j].unpack(z[j]);
     }
-    if (row + gridDim.x < a.T) fetch(row + gridDim.x);
+    if (kAhead && next < a.T) fetch(next);
+    if (!kAhead && next < a.T) {
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        if (c0 + j * step >= a.d) continue;
+        const int64_t at = int64_t(next) * a.d + c0 + j * step;
+        prefetch_l2(residual + at);
+        if (y) prefetch_l2(y + at);
+      }
+    }
     if (y) {
       float scale = a.alpha;  // times the post-norm's 1 / rms
       if (a.w_post) {
@@ -152,9 +168,12 @@ __global__ void __launch_bounds__(kResident, 1) k_block_norm(NormArgs a) {
 }  // namespace
 
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
-  // the fewest whole warps of eight elements a lane, up to 16 warps (and 32 past 8192 elements); fewer
-  // warps with more elements a lane are slower (8 -> 4 warps at 2048: 46.1 -> 47.7 us)
-  const int threads = a.d > 8192 ? 1024 : std::min(512, (a.d / 8 + 31) / 32 * 32);
+  // The fewest whole warps of eight elements a lane: fewer with more elements a lane are slower (8 -> 4
+  // warps at 2048: 46.1 -> 47.7 us; 2 -> 1 at 512: 13.1 -> 13.9).  Past 4096 elements two CTAs of 16
+  // warps with 16 elements a lane are better where both inputs are bf16 (1831 rows of 8192: 23.0 us, one
+  // of 32 warps 27.6), one CTA of up to 32 with eight where one is fp32 (1464 rows: 24.9 against 28.8).
+  const int most = a.y_bf16 && a.r_bf16 && a.d <= 8192 ? 512 : 1024;
+  const int threads = std::min(most, (a.d / 8 + 31) / 32 * 32);
   auto by_type = [](bool bf16, auto f) { return bf16 ? f(__nv_bfloat16{}) : f(float{}); };
   auto go = [&](auto v) {
     constexpr int kVecs = decltype(v)::value;

@@ -586,6 +586,22 @@ def test_block_norm_parts(moe):
     assert moe.block_norm(rd[:0], w.cuda(), y=rd[:0])[1].shape == (0, 2048)
 
 
+@pytest.mark.parametrize("d", [264, 4104, 6200, 8192, 10000, 16384])
+@pytest.mark.parametrize("ty,tr", [(BF, BF), (F32, BF), (BF, F32), (F32, F32)])
+def test_block_norm_rows_in_turn(moe, d, ty, tr):
+    """More rows than run at once, in place: a row is read ahead of its turn and written in it."""
+    g = gen(d)
+    T = 5000 if d == 264 else 331
+    y, r = (2 * torch.randn(T, d, generator=g)).to(ty), (3 * torch.randn(T, d, generator=g)).to(tr)
+    w_pre, w_post = 1 + 0.2 * torch.randn(d, generator=g), 1 + 0.2 * torch.randn(d, generator=g)
+    want_r, want_x, tol_r, tol_x = o.block_norm(y, w_post, None, 0.6, r, w_pre, 1e-5, tr, BF)
+    r_dev = r.cuda()
+    r_out, x = moe.block_norm(r_dev, w_pre.cuda(), y=y.cuda(), w_post=w_post.cuda(), alpha=0.6, eps=1e-5, x_dtype=BF)
+    assert r_out is r_dev
+    close(r_out, want_r, tol_r, f"d {d} residual")
+    close(x, want_x, tol_x, f"d {d} x")
+
+
 def test_binding_refuses_tensors_that_do_not_fit(moe):
     cache = moe.KVCache.empty(4, 2, 16, 64)
     ws = moe.attn_workspace(cache, 4, 2)
