@@ -27,26 +27,26 @@
 // goes on.  Four warps add up the results of the groups that had a tile of the segment, write the
 // output or the partial result, and join partial results.  So neither the copies nor the products
 // wait for a segment's end (with all of that in the eight warps, 128 windows of 513 tokens took
-// 31.4 us, like this 21.3).  A group passes over segments without a tile of its own, so that several
+// 31.4 us, like this 22.3).  A group passes over segments without a tile of its own, so that several
 // short ones are worked on at once, each group with a join buffer of its own (177 sequences of up to
 // 42 tokens, 8 kv heads of 8 query heads, 192 wide, E4M3: with all eight warps at every segment's
-// end and one warp for the queries 79 us, like this 43).  A stage, and a join buffer, belongs to one
+// end and one warp for the queries 79 us, with this 43, and 48 with the E4M3 form's small weights).  A stage, and a join buffer, belongs to one
 // group: a barrier's wait tells only the parity of the phase, so whoever waits for it has to have seen
 // each of its phases.
 //
 // Code is short where it can be: sixteen warps run six programs, and where segments are short the
 // instruction cache does not hold them.  So a tile's whole and its masked rows go one way (two copies of
-// the product code, one without masks, gained 1 % on long rows, and cost 68 us against 43 there, and
-// 88 against 62 for 52 mixed lengths of up to 499 tokens, groups of 12, 256 wide).
+// the product code, one without masks, gained 1 % on long rows, and cost 67 us against that 43, and
+// 87 against 62 for 52 mixed lengths of up to 499 tokens, groups of 12, 256 wide).
 //
 // Starting a copy holds a warp up for 100 to 200 cycles, enough to fall behind the memory with the 2 KB
 // copies of 16-token pages if it computes anything else there: there is no division a tile, each lane
 // has its own copy of every tile worked out beforehand, and the copies of a tile are shared out between
-// the two warps (32 mixed lengths, E4M3: one warp 22.8 us, two 20.8).
+// the two warps (32 mixed lengths, E4M3: one warp 22.8 us, two 20.5).
 //
 // Measured (GB300, bf16 unless said, 4 kv heads of 4 query heads, 128 wide): 64 sequences of up to 16k
 // tokens 200 us, 1.37 GB at the measured copy rate; one of 64k tokens 28.9 us (69 % of that rate); one
-// 513-token window 6.8 us, all of it latency (the lengths, the pages, the tile, the count of partial
+// 513-token window 7.1 us, all of it latency (the lengths, the pages, the tile, the count of partial
 // results and their joint are each a trip to memory).  What a call costs beyond its bytes is about
 // 10 us: 3 to 4 until the first tile is there, 4 from the last tile to the end, and the launch.
 //
@@ -521,9 +521,13 @@ struct WarpBf16 {
 // 2h holds the hi of head h, column 2h + 1 its lo, so lane (g, t) has both products of head t and
 // adds them up.
 //
-// The smallest step of the split is 2^-22 of the largest weight, so the weights are taken relative
-// to the maximum over the warp's own 32 tokens, and the product is added to the accumulator by an
-// fp32 factor: a long row of small weights keeps its precision beside a large one.
+// The weights are taken relative to the maximum over the warp's own 32 tokens, and the product is added
+// to the accumulator by an fp32 factor: a long row of small weights keeps its precision beside a large
+// one.  The split holds the 2^-8 down to 2^-15 of that maximum; where weights are smaller (and not 0),
+// they take a product of their own, 2^15 times as large, and so on, down to 2^-75 of it.  (They matter
+// where the large weights meet values of 0.)  With one product for all weights of a tile 64 sequences of
+// up to 8k tokens, groups of 8, took 68.9 us, like this 79.2.  The products are a loop, not copies: see
+// above on the size of the code (d 256: 77 us against 68).
 //
 // The values' codes: a register of ldmatrix with transpose holds elements 2g and 2g + 1 of tokens 2t
 // and 2t + 1; a byte permutation of it and the one of tokens 2t + 8 and 2t + 9 gives the four
@@ -532,6 +536,13 @@ struct WarpBf16 {
 template <typename S>
 struct WarpE4M3 {
   static constexpr int kKS = S::kDim / 32, kNB = S::kHeads / 4, kMD = S::kDim / 16;
+  // of 256 times the weights: the least that the split holds, and the factor of the next product; how many
+  // products leave weights to another
+  static constexpr float kLeast = 1.0f / 128.0f, kLift = 32768.0f;
+  static constexpr int kRounds = 4;
+  static __device__ __forceinline__ bool below_least(float x) {  // and above 0 (no weight is negative)
+    return __float_as_uint(x) - 1u < __float_as_uint(kLeast) - 1u;
+  }
   static_assert(S::kPerWarp == 32, "the 32 tokens of one product with the values");
   uint32_t q[kKS][kNB][2];
   float m[kNB], sum[kNB], factor[kNB], acc[kMD][kNB][2];
@@ -671,48 +682,80 @@ struct WarpE4M3 {
         for (int md = 0; md < kMD; ++md) acc[md][nb][0] *= fix, acc[md][nb][1] *= fix;
       }
     }
-    uint32_t w[kNB][2];
     float into[kNB];  // of the product, in the accumulator: 2^-8 for the 256
+    bool small = false;  // weights that are too small for the split beside the largest
 #pragma unroll
     for (int nb = 0; nb < kNB; ++nb) {
       const float f = m[nb] == -INFINITY ? 0.0f : exp2_fast(base[nb] - m[nb]);
       float all = 0.0f;
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const float p0 = exp2_fast(s[mt][nb][0] - base[nb]), p1 = exp2_fast(s[mt][nb][1] - base[nb]);
-        all += p0 + p1;
-        const float w0 = p0 * unit[mt][0] * 256.0f, w1 = p1 * unit[mt][1] * 256.0f;
-        const uint32_t hi = e4m3_code2(w0, w1);
-        const float2 f2 = float2_of_codes(hi);
-        const uint32_t lo = e4m3_code2((w0 - f2.x) * 32.0f, (w1 - f2.y) * 32.0f);
-        w[nb][mt] = transpose8x8(hi | lo << 16);
-      }
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float& x = s[mt][nb][half];
+          x = exp2_fast(x - base[nb]);
+          all += x;
+          x *= unit[mt][half] * 256.0f;
+          small |= below_least(x);
+        }
       sum[nb] = fmaf(all, f, sum[nb]);
       into[nb] = f * (1.0f / 256.0f);
     }
+    bool rest = __any_sync(0xffffffffu, small);
+#pragma unroll 1
+    for (int round = 1;; ++round) {
+      uint32_t w[kNB][2];
 #pragma unroll
-    for (int i = 0; i < kKS; ++i) {
-      uint32_t r[2][4];
+      for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        ldmatrix4_trans(rows(tv.v, mt, i), r[mt]);
-      }
+        for (int mt = 0; mt < 2; ++mt) {
+          // what is too small waits for the next round
+          const float w0 = rest && s[mt][nb][0] < kLeast ? 0.0f : s[mt][nb][0];
+          const float w1 = rest && s[mt][nb][1] < kLeast ? 0.0f : s[mt][nb][1];
+          const uint32_t hi = e4m3_code2(w0, w1);
+          const float2 f2 = float2_of_codes(hi);
+          const uint32_t lo = e4m3_code2((w0 - f2.x) * 32.0f, (w1 - f2.y) * 32.0f);
+          w[nb][mt] = transpose8x8(hi | lo << 16);
+        }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // element 2g of tokens 2t, 2t + 8, 2t + 1, 2t + 9 (row g of the operand), and 2g + 1 (row g + 8)
-        const uint32_t a0 = __byte_perm(r[0][2 * h], r[0][2 * h + 1], 0x6240);
-        const uint32_t a1 = __byte_perm(r[0][2 * h], r[0][2 * h + 1], 0x7351);
-        const uint32_t a2 = __byte_perm(r[1][2 * h], r[1][2 * h + 1], 0x6240);
-        const uint32_t a3 = __byte_perm(r[1][2 * h], r[1][2 * h + 1], 0x7351);
+      for (int i = 0; i < kKS; ++i) {
+        uint32_t r[2][4];
 #pragma unroll
-        for (int nb = 0; nb < kNB; ++nb) {
-          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_e4m3_16x8x32(d, a0, a1, a2, a3, w[nb][0], w[nb][1]);
-          float(&o)[2] = acc[2 * i + h][nb];
-          o[0] = fmaf(fmaf(d[1], 1.0f / 32.0f, d[0]), into[nb], o[0]);
-          o[1] = fmaf(fmaf(d[3], 1.0f / 32.0f, d[2]), into[nb], o[1]);
+        for (int mt = 0; mt < 2; ++mt) {
+          ldmatrix4_trans(rows(tv.v, mt, i), r[mt]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // element 2g of tokens 2t, 2t + 8, 2t + 1, 2t + 9 (row g of the operand), and 2g + 1 (row g + 8)
+          const uint32_t a0 = __byte_perm(r[0][2 * h], r[0][2 * h + 1], 0x6240);
+          const uint32_t a1 = __byte_perm(r[0][2 * h], r[0][2 * h + 1], 0x7351);
+          const uint32_t a2 = __byte_perm(r[1][2 * h], r[1][2 * h + 1], 0x6240);
+          const uint32_t a3 = __byte_perm(r[1][2 * h], r[1][2 * h + 1], 0x7351);
+#pragma unroll
+          for (int nb = 0; nb < kNB; ++nb) {
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_e4m3_16x8x32(d, a0, a1, a2, a3, w[nb][0], w[nb][1]);
+            float(&o)[2] = acc[2 * i + h][nb];
+            o[0] = fmaf(fmaf(d[1], 1.0f / 32.0f, d[0]), into[nb], o[0]);
+            o[1] = fmaf(fmaf(d[3], 1.0f / 32.0f, d[2]), into[nb], o[1]);
+          }
         }
       }
+      if (!rest) break;
+      small = false;
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb) {
+        into[nb] *= 1.0f / kLift;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            float& x = s[mt][nb][half];
+            x = x < kLeast ? x * kLift : 0.0f;
+            small |= below_least(x);
+          }
+      }
+      rest = round < kRounds && __any_sync(0xffffffffu, small);
     }
   }
 

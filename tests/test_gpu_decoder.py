@@ -316,6 +316,19 @@ def test_attention_many_short_sequences(moe, e4m3):
     check_attention(moe, 78, lens.tolist(), 2, 1, 64, 16, e4m3, poison=False)
 
 
+@pytest.mark.parametrize("dim,heads,kv_heads", [(64, 12, 4), (128, 16, 4), (128, 32, 2), (192, 24, 4), (256, 20, 4)])
+@pytest.mark.parametrize("window", [0, 45])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_short_sequences_side_by_side(moe, dim, heads, kv_heads, window, e4m3):
+    """Several segments of one or a few tiles a CTA, a different number of tiles each, some cut between
+    two CTAs, and rows in every tile that are not seen and hold no numbers."""
+    g = gen(dim + heads + window)
+    lens = torch.randint(1, 150, (180,), generator=g)
+    lens[::17] = 0
+    lens[5], lens[60], lens[179] = 700, 1, 333
+    check_attention(moe, 90 + dim, lens.tolist(), heads, kv_heads, dim, 48, e4m3, window=window)
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_attention_nan_stays_in_its_head(moe, e4m3):
     """A query with a NaN or an infinity, and a key row with a NaN, spoil their heads and no other."""
