@@ -30,9 +30,9 @@
 // 31.4 us, like this 22.3).  A group passes over segments without a tile of its own, so that several
 // short ones are worked on at once, each group with a join buffer of its own (177 sequences of up to
 // 42 tokens, 8 kv heads of 8 query heads, 192 wide, E4M3: with all eight warps at every segment's
-// end and one warp for the queries 79 us, with this 43, and 48 with the E4M3 form's small weights).  A stage, and a join buffer, belongs to one
-// group: a barrier's wait tells only the parity of the phase, so whoever waits for it has to have seen
-// each of its phases.
+// end and one warp for the queries 79 us, with this 43, and 48 with the E4M3 form's small weights).
+// A stage, and a join buffer, belongs to one group: a barrier's wait tells only the parity of the
+// phase, so whoever waits for it has to have seen each of its phases.
 //
 // Code is short where it can be: sixteen warps run six programs, and where segments are short the
 // instruction cache does not hold them.  So a tile's whole and its masked rows go one way (two copies of
