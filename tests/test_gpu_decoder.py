@@ -367,6 +367,36 @@ def test_attention_sharp_and_scaled_rows(moe, e4m3):
     check_attention(moe, 16, [300, 64], 8, 2, 128, 16, e4m3, q_size=1e15, scale=1e-15)
 
 
+@pytest.mark.parametrize("dim,heads", [(64, 5), (128, 4), (128, 8), (256, 3)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_attention_small_weights_alone_in_their_elements(moe, dim, heads, e4m3):
+    """Weights of six sizes down to e^-48, side by side in every tile, each with elements in which no
+    other token has a value: every size keeps its own precision."""
+    g = gen(5)
+    n, page = 200, 16
+    level = torch.arange(n) % 6
+    k = torch.tensor([0.0, -11.0, -20.0, -30.0, -40.0, -48.0])[level][:, None].expand(n, dim)
+    v = torch.randn(n, dim, generator=g) * (torch.arange(dim) % 6 == level[:, None])
+    n_pages = -(-n // page)
+    pools = [torch.cat([x, torch.zeros(n_pages * page - n, dim)]).view(n_pages, 1, page, dim).to(BF) for x in (k, v)]
+    exps = [None, None]
+    if e4m3:
+        codes, exps = zip(*[o.quantise(x) for x in pools])
+        pools = [c.float().to(torch.float8_e4m3fn).view(torch.uint8) for c in codes]
+    pools = [*pools, *exps]
+    q = torch.ones(1, heads, dim).to(BF)
+    table = torch.randperm(n_pages, generator=g)
+    pools = [t if t is None else t[torch.argsort(table)] for t in pools]
+    table, lens = table.int().view(1, -1), torch.tensor([n], dtype=torch.int32)
+    want, lse, tol, tol_lse = o.attention(q, *pools, lens, table, 1 / dim, 0)
+    cache = to_device(moe, pools)
+    ws = moe.attn_workspace(cache, heads, 1)
+    got_lse = torch.empty(1, heads, device="cuda")
+    out = moe.attn_decode(q.cuda(), cache, lens.cuda(), table.cuda(), ws, scale=1 / dim, lse=got_lse)
+    close(out, want, tol, "out")
+    close(got_lse, lse, tol_lse, "lse")
+
+
 def test_attention_scores_of_minus_infinity_and_rows_of_zeros(moe):
     """Keys that give -infinity are masked tokens; with nothing else the row is empty.  E4M3 rows of zeros
     (the smallest exponent) beside others, and nothing but them."""
