@@ -55,6 +55,7 @@
 // padded to; a tcgen05 product has at least 64 rows on M, and its scores would have to travel
 // through TMEM.  Keys and values reach the registers by ldmatrix from the swizzled tiles, the
 // values transposed.
+#include "batches.cuh"
 #include "decoder.cuh"
 #include "tcgen05.cuh"
 
@@ -208,6 +209,15 @@ __device__ __forceinline__ float sum_over_rows(float v) {
   return v;
 }
 __device__ __forceinline__ void end_sync() { named_bar_sync(1, kEndThreads); }  // of the warps that end segments
+__device__ __forceinline__ bool end_all(bool ok) {  // end_sync, and whether `ok` holds for all of them
+  int all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(int(ok)), "n"(kEndThreads)
+      : "memory");
+  return all != 0;
+}
 template <int kRegs>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -796,10 +806,12 @@ struct Joint {
 // Joins them, by the kEndThreads threads that end segments.  The slots are copied to `stage` (room for
 // `stage_bytes`) by bulk copies, all at once or as many as fit, their start spread over the warps
 // (starting one takes 100 to 200 cycles).  For 38 slots, loads to registers take several rounds to L2
-// (4.8 us), and 16-byte cp.async copies 8 us.  `round` counts the uses of the barrier.
+// (4.8 us), and 16-byte cp.async copies 8 us.  Each warp arrives with the bytes of its own copies.
+// `round` counts the uses of the barrier; `ok` is whether all went well so far for the thread, and
+// without that nothing is written.
 template <typename S>
 __device__ __forceinline__ bool join_partials(const AttnArgs& a, const float* slots, const Joint& j, uint8_t* stage,
-                                              int stage_bytes, int tid, uint64_t* bar, int& round, int* abort) {
+                                              int stage_bytes, int tid, uint64_t* bar, int& round, bool ok) {
   constexpr int kEach = (S::kHeads * S::kDim / 4 + kEndThreads - 1) / kEndThreads;  // items (4 elements) a thread
   const int row_items = a.cache.dim / 4, items = j.heads * row_items;
   const int bytes = (2 * S::kHeads + j.heads * S::kDim) * 4;
@@ -810,17 +822,20 @@ __device__ __forceinline__ bool join_partials(const AttnArgs& a, const float* sl
     top[e] = -INFINITY;
     all[e] = v[e][0] = v[e][1] = v[e][2] = v[e][3] = 0.0f;
   }
-  bool ok = true;
-  for (int i0 = 0; i0 < j.n; i0 += batch, ++round) {
-    const int n = min(batch, j.n - i0);
-    if (tid == 0) mbar_arrive_expect_tx(bar, n * bytes);
-    end_sync();  // the stage is free
-    for (int k = tid / 32 + kEndThreads / 32 * (tid % 32); k < n; k += kEndThreads) {
+  constexpr int kEndWarps = kEndThreads / 32;
+  auto start = [&](int i0, int n) {
+    const int w = tid / 32;
+    if (tid % 32 == 0) mbar_arrive_expect_tx(bar, (n - w + kEndWarps - 1) / kEndWarps * bytes);  // n - w >= -2
+    __syncwarp();
+    for (int k = w + kEndWarps * (tid % 32); k < n; k += kEndThreads) {
       const int i = i0 + k;
       bulk_g2s(stage + k * bytes, slots + (size_t(j.c0 + i) * 2 + (i == 0)) * S::kSlot, bytes, bar);
     }
     __syncwarp();
-    ok = wait(bar, round & 1, abort) && ok;
+  };
+  // not cut short by the CTA's `abort`: the copies are under way, and have to land before the CTA ends
+  auto landed = [&] { return mbar_wait_copies(bar, round++ & 1); };
+  auto use = [&](int, int n) {
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int item = tid + e * kEndThreads;
@@ -845,7 +860,9 @@ __device__ __forceinline__ bool join_partials(const AttnArgs& a, const float* sl
         v[e][3] = fmaf(x.w, f, v[e][3]);
       }
     }
-  }
+  };
+  ok = in_batches(j.n, batch, ok, end_all, start, landed, use);
+  if (!ok) return false;
 #pragma unroll
   for (int e = 0; e < kEach; ++e) {
     const int item = tid + e * kEndThreads;
@@ -856,7 +873,7 @@ __device__ __forceinline__ bool join_partials(const AttnArgs& a, const float* sl
         make_uint2(pack_bf16x2(v[e][0] * scale, v[e][1] * scale), pack_bf16x2(v[e][2] * scale, v[e][3] * scale));
     if (d == 0 && a.lse) a.lse[j.row + h] = all[e] == 0.0f ? -INFINITY : top[e] * kLn2 + logf(all[e]);
   }
-  return ok;
+  return true;
 }
 
 template <int... I, typename F>
@@ -894,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->join_full[i], S::kGroupWarps);
       mbar_init(&ctl->join_empty[i], kEndThreads / 32);
     }
-    mbar_init(&ctl->merge_full, 1);
+    mbar_init(&ctl->merge_full, kEndThreads / 32);
     ctl->abort = 0;
     mbar_fence_init();
     prefetch_map(&map_k);
@@ -1115,7 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++joins;
       });
     }
-    if (timed_out && lane == 0) report_timeout_flag(a.table.status_flags, 42);
+    if (timed_out) report_timeout_flag(a.table.status_flags, 42);  // any lane: each waits for itself
     return;
   }
 
@@ -1216,14 +1233,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n_joints++ == 0) joints[0] = joints[1];
     }
   }
-  // The ring is free by now: every tile has been used.  (A part has at most two segments that it shares.)
+  // The ring is free by now: every tile has been used, or a wait ran out, and nothing is joined.  (A part
+  // has at most two segments that it shares.)
+  bool ok = !timed_out;
   int round = 0;
 #pragma unroll 1
   for (int i = 0; i < n_joints; ++i)
-    if (!join_partials<S>(a, reinterpret_cast<const float*>(a.ws + kAttnPartialsAt), i == 0 ? joints[0] : joints[1], smem,
-                          int(S::kExpsAt), tid, &ctl->merge_full, round, &ctl->abort))
-      timed_out = true;
-  if (timed_out && lane == 0) report_timeout_flag(a.table.status_flags, 43);
+    ok = join_partials<S>(a, reinterpret_cast<const float*>(a.ws + kAttnPartialsAt), i == 0 ? joints[0] : joints[1], smem,
+                          int(S::kExpsAt), tid, &ctl->merge_full, round, ok);
+  if (timed_out || !ok) report_timeout_flag(a.table.status_flags, 43);  // any lane
 }
 
 // -------------------------------------------------------------------------- host ------------

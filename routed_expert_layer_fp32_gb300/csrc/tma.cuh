@@ -67,6 +67,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// Wait for copies under way, whatever became of the other warps; false after kWaitLimitNs.
+__device__ __forceinline__ bool mbar_wait_copies(uint64_t* bar, uint32_t parity) {
+  unsigned long long t0 = 0;  // (the clock takes longer to read than most copies to land)
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 63u) {
+      if (t0 == 0) t0 = global_timer_ns();
+      else if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+    }
+  }
+}
+
 // ---- thread-block cluster helpers (distributed shared memory) ----
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
