@@ -218,8 +218,9 @@ moe_status moe_forward_stack_traced(const moe_layer* layers, int L, void* residu
                                     unsigned flags, void* ws, size_t ws_bytes, moe_stream_t stream,
                                     moe_event_t* events);
 
-/* Synchronises `stream`, returns the first device-side error recorded in the workspace
- * since the last call (MOE_OK if none) and clears the record. */
+/* Synchronises `stream`, returns a device-side error recorded in the workspace since the last
+ * call (MOE_OK if none; of several MOE_ERR_INDEX before MOE_ERR_TIMEOUT, and that before refused
+ * ids and pages) and clears the record. */
 moe_status moe_get_status(void* ws, moe_stream_t stream);
 
 /* moe_route without a workspace, for callers that cannot allocate device memory (a host

@@ -328,9 +328,11 @@ moe_status moe_get_status(void* ws, moe_stream_t stream) {
   if (cudaMemcpy(&h, ws, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
   if (cudaMemset(ws, 0, sizeof(DevStatus)) != cudaSuccess) return MOE_ERR_CUDA;
   if (h.flags & kFlagIndex) return MOE_ERR_INDEX;
+  // one code of those recorded: a timeout before refused ids and pages, as only after it is there no result,
+  // and an attention workspace to be initialised again
+  if (h.flags & kFlagTimeout) return MOE_ERR_TIMEOUT;
   if (h.flags & kFlagBadForced) return MOE_ERR_BAD_FORCED_ID;
   if (h.flags & kFlagBadPage) return MOE_ERR_BAD_PAGE;
-  if (h.flags & kFlagTimeout) return MOE_ERR_TIMEOUT;
   return MOE_OK;
 }
 
