@@ -17,6 +17,8 @@ from .binding import MOE_BF16, MOE_E4M3, MOE_F32
 _CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 # the current stream's handle alone: 0.1 us, a torch.cuda.Stream 3 us (absent from builds without CUDA)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_devices = 0  # of the process; 0: not counted yet
 
 
 class MoeKvCacheC(ctypes.Structure):
@@ -74,8 +76,20 @@ def _misfit(name: str, t: torch.Tensor, what: str):
                       f"{list(t.stride())} on {t.device}")
 
 
+def _check_device(dev: int):
+    """The library launches on the current device, and handle 0, the default stream, is that device's own:
+    a call on another device's tensors would run here with that one's addresses.  (Asking for the current
+    device takes 0.4 us, so calls ask only where there are several.)"""
+    global _devices
+    if _devices == 0:
+        _devices = torch.cuda.device_count()
+    if _devices != 1 and dev != _current_device():
+        raise ValueError(f"the tensors are on GPU {dev}, not on the current one: call under torch.cuda.device({dev})")
+
+
 def attn_workspace(cache: KVCache, n_heads: int, B: int) -> torch.Tensor:
     """Workspace of attn_decode for up to B sequences (kept by the caller, one call at a time)."""
+    _check_device(cache.device)
     n = int(_b.lib().moe_attn_workspace_bytes(cache.ref, n_heads, B))
     if n == 0:
         raise _b.MoeError(-2, "moe_attn_workspace_bytes")
@@ -119,6 +133,8 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, cache: KVCache, pos: torch.Tensor
     """Writes tokens' keys and values, k and v [T, n_kv_heads, head_dim] bf16 or fp32 (rows may be
     slices of a fused projection's output), at position pos[t] of sequence seq[t] (None: t)."""
     T, dev, heads, dim = k.shape[0], cache.device, cache.n_kv_heads, cache.head_dim
+    if _devices != 1:
+        _check_device(dev)
     code, shape = _CODES.get(k.dtype), (T, heads, dim)
     if code is None or k.shape != shape or k.get_device() != dev:
         raise _misfit("k", k, f"bf16 or fp32 {list(shape)}")
@@ -137,6 +153,8 @@ def kv_read(cache: KVCache, pos: torch.Tensor, page_table: torch.Tensor, ws: tor
     """The keys and values at position pos[t] of sequence seq[t] (None: t): (k, v), each
     [T, n_kv_heads, head_dim] of `dtype`, or of the given output tensors."""
     T, dev = pos.shape[0], cache.device
+    if _devices != 1:
+        _check_device(dev)
     shape = (T, cache.n_kv_heads, cache.head_dim)
     if k is None:
         k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=cache.k.device)
@@ -163,6 +181,8 @@ def attn_decode(q: torch.Tensor, cache: KVCache, lens: torch.Tensor, page_table:
     defaults to head_dim ** -0.5.  Returns out [B, n_heads, head_dim] bf16; lse [B, n_heads] fp32,
     where given, receives the log-sum-exp of the scores."""
     dev, dim, shape = cache.device, cache.head_dim, q.shape
+    if _devices != 1:
+        _check_device(dev)
     if q.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != dim or q.get_device() != dev:
         raise _misfit("q", q, f"bf16 [sequences, n_heads, {dim}]")
     B, H, _ = shape
@@ -199,6 +219,8 @@ def block_norm(residual: torch.Tensor, w_pre: Optional[torch.Tensor], y: Optiona
     shape, dev, code = residual.shape, residual.get_device(), _CODES.get(residual.dtype)
     if dev < 0 or code is None or len(shape) != 2 or not residual.is_contiguous():
         raise _misfit("residual", residual, "bf16 or fp32 [tokens, d], contiguous and on a GPU")
+    if _devices != 1:
+        _check_device(dev)
     T, d = shape
     rp = residual.data_ptr()
     yp, y_code, post, pre, gp, gs, g_code, xp, x_code = None, 0, None, None, None, 0, 0, None, 0
