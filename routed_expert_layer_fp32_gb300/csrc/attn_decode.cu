@@ -1267,15 +1267,21 @@ bool cache_map(CUtensorMap* map, const void* base, const CacheDev& c, int box, i
 template <typename S>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   const CacheDev& c = a.cache;
-  static const cudaError_t attr = [] {
+  static std::atomic<int> ready[kMaxDevices];
+  cudaError_t attr = cudaSuccess;
+  once_a_device(ready, current_device(), [&attr] {
     cudaFuncAttributes f;
-    cudaError_t e = cudaFuncGetAttributes(&f, k_attn_decode<S>);
-    if (e != cudaSuccess) return e;
+    attr = cudaFuncGetAttributes(&f, k_attn_decode<S>);
     // the warpgroups divide up what the launch gets: with less than they ask for they would wait for ever
-    if (4 * f.numRegs < 2 * kComputeRegs + kProducerRegs + kEndRegs) return cudaErrorInvalidConfiguration;
-    return cudaFuncSetAttribute(k_attn_decode<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
-  }();
+    if (attr == cudaSuccess && 4 * f.numRegs < 2 * kComputeRegs + kProducerRegs + kEndRegs)
+      attr = cudaErrorInvalidConfiguration;
+    if (attr == cudaSuccess)
+      attr = cudaFuncSetAttribute(k_attn_decode<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
+    return int(attr == cudaSuccess);
+  });
   if (attr != cudaSuccess) return attr;
+  const int ctas = std::min(sm_count(), kMaxCtas);
+  if (ctas <= 0) return cudaErrorInvalidDevice;
   // tokens a copy: the largest power of two that divides a page, up to a tile
   const int box = std::min(S::kTokens, c.page & -c.page);
   const int spans = c.dim % S::kSpanElems == 0 ? S::kSpans : 1;  // of a row in one copy
@@ -1286,7 +1292,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   // i / page_boxes = the high half of i * page_magic, for i below 2^32 / page_boxes: positions below 2^28
   // make at most 2^24 boxes of 16, and a page at most 256
   const uint32_t page_magic = uint32_t(((uint64_t(1) << 32) + page_boxes - 1) / page_boxes);
-  return launch_pdl(k_attn_decode<S>, dim3(std::min(sm_count(), kMaxCtas)), dim3(kThreads), S::kSmem, s, a, mk, mv, box,
+  return launch_pdl(k_attn_decode<S>, dim3(ctas), dim3(kThreads), S::kSmem, s, a, mk, mv, box,
                     S::kSpans / spans, page_boxes, page_magic, group, (group + S::kHeads - 1) / S::kHeads);
 }
 

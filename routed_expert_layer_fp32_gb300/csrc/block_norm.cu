@@ -175,9 +175,11 @@ cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s) {
   const int most = a.y_bf16 && a.r_bf16 && a.d <= 8192 ? 512 : 1024;
   const int threads = std::min(most, (a.d / 8 + 31) / 32 * 32);
   auto by_type = [](bool bf16, auto f) { return bf16 ? f(__nv_bfloat16{}) : f(float{}); };
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
   auto go = [&](auto v) {
     constexpr int kVecs = decltype(v)::value;
-    const dim3 grid(std::min(a.T, sm_count() * (kResident / threads)));
+    const dim3 grid(std::min(a.T, sms * (kResident / threads)));
     return by_type(a.y_bf16, [&](auto y) {
       return by_type(a.r_bf16, [&](auto r) {
         return by_type(a.x_bf16, [&](auto x) {

@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "per_device.cuh"
 
 namespace moe {
 
@@ -79,14 +80,18 @@ __device__ __forceinline__ void store_vec8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+inline int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
 inline int sm_count() {
-  static const int sms = [] {
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
-  }();
-  return sms;
+  static std::atomic<int> kept[kMaxDevices];
+  const int dev = current_device();
+  return once_a_device(kept, dev, [dev] {
+    int n = 0;
+    return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? n : 0;
+  });
 }
 
 // Workspace of the attention: the status record, then the join counters and partial results of
