@@ -6,7 +6,8 @@
 // with the running maximum m, the sum and the accumulator in fp32.  In an E4M3 cache key j is
 // 2^a_j times its codes and value j is 2^c_j times its codes: 2^a_j multiplies the score, and the
 // weight of value j's codes is w_j = p_j 2^c_j; there m is the maximum of t_j + c_j, so that no w_j
-// is above 1 and the largest is close to it, however the rows' sizes differ.
+// is above 1 and the largest is close to it, however the rows' sizes differ.  p_j itself may then be
+// anything from 2^-120 (beside values of the largest size) to 2^100 (kMinExp): see kAbove and scale_sum.
 //
 // What bounds it is reading the cache: 2 * group operations an element (group = query heads a kv
 // head), against about 290 a byte for the tensor cores.  So the kernel is built around keeping
@@ -197,6 +198,20 @@ __device__ __forceinline__ bool wait_part(uint64_t* bar, uint32_t parity, int* a
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// `sum` times 2^d, d <= 0; returns 2^d.  In the E4M3 form 2^d may be too small for a float where the sum it
+// scales is large: in two steps of 2^(d / 2).
+template <typename S>
+__device__ __forceinline__ float scale_sum(float& sum, float d) {
+  if constexpr (S::kE4M3) {
+    const float half = exp2_fast(0.5f * d);
+    sum = sum * half * half;
+    return half * half;
+  } else {
+    const float f = exp2_fast(d);
+    sum *= f;
+    return f;
+  }
 }
 __device__ __forceinline__ float max_over_rows(float v) {  // over the lanes that share lane % 4
 #pragma unroll
@@ -550,6 +565,9 @@ struct WarpE4M3 {
   // products leave weights to another
   static constexpr float kLeast = 1.0f / 128.0f, kLift = 32768.0f;
   static constexpr int kRounds = 4;
+  // Factors are taken 2^24 times as large, as exp2 gives no numbers below 2^-126, and the largest of a tile
+  // may be 2^-120 (values of 2^128); at the other end there is room (2^100).
+  static constexpr float kAbove = 24.0f;
   static __device__ __forceinline__ bool below_least(float x) {  // and above 0 (no weight is negative)
     return __float_as_uint(x) - 1u < __float_as_uint(kLeast) - 1u;
   }
@@ -673,30 +691,30 @@ struct WarpE4M3 {
           top[nb] = fmaxf(top[nb], x + c);
         }
       }
-    float base[kNB], now[kNB];  // the maximum over these tokens, and over all so far
+    float base[kNB], now[kNB];  // the maximum over these tokens, less kAbove, and over all so far
     bool moved = false;
 #pragma unroll
     for (int nb = 0; nb < kNB; ++nb) {
       const float here = max_over_rows(top[nb]);
       now[nb] = fmaxf(m[nb], here);
       moved |= now[nb] != m[nb];
-      base[nb] = here == -INFINITY ? 0.0f : here;
+      base[nb] = here == -INFINITY ? 0.0f : here - kAbove;
     }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
       for (int nb = 0; nb < kNB; ++nb) {
-        const float fix = now[nb] == -INFINITY ? 0.0f : exp2_fast(m[nb] - now[nb]);
+        const float fix = scale_sum<S>(sum[nb], now[nb] == -INFINITY ? 0.0f : m[nb] - now[nb]);
         m[nb] = now[nb];
-        sum[nb] *= fix;
 #pragma unroll
         for (int md = 0; md < kMD; ++md) acc[md][nb][0] *= fix, acc[md][nb][1] *= fix;
       }
     }
-    float into[kNB];  // of the product, in the accumulator: 2^-8 for the 256
+    float into[kNB];  // of the product, in the accumulator: 2^-8 for the 256 times the weights
     bool small = false;  // weights that are too small for the split beside the largest
 #pragma unroll
     for (int nb = 0; nb < kNB; ++nb) {
-      const float f = m[nb] == -INFINITY ? 0.0f : exp2_fast(base[nb] - m[nb]);
+      // the factors' 2^(base - m), in two halves as in scale_sum; at most 2^-kAbove, also where nothing is seen
+      const float half_f = exp2_fast(fminf(0.5f * (base[nb] - m[nb]), -0.5f * kAbove));
       float all = 0.0f;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
@@ -705,11 +723,11 @@ struct WarpE4M3 {
           float& x = s[mt][nb][half];
           x = exp2_fast(x - base[nb]);
           all += x;
-          x *= unit[mt][half] * 256.0f;
+          x *= unit[mt][half] * (256.0f * 0x1p-24f);  // 256 times the weight
           small |= below_least(x);
         }
-      sum[nb] = fmaf(all, f, sum[nb]);
-      into[nb] = f * (1.0f / 256.0f);
+      sum[nb] = fmaf(all * half_f, half_f, sum[nb]);
+      into[nb] = half_f * (0x1p24f / 256.0f) * half_f;
     }
     bool rest = __any_sync(0xffffffffu, small);
 #pragma unroll 1
@@ -844,16 +862,16 @@ __device__ __forceinline__ bool join_partials(const AttnArgs& a, const float* sl
       const float before = top[e];
       for (int k = 0; k < n; ++k) top[e] = fmaxf(top[e], *reinterpret_cast<const float*>(stage + k * bytes + h * 4));
       const float base = top[e] == -INFINITY ? 0.0f : top[e];
-      const float fix = exp2_fast(before - base);
-      all[e] *= fix;
+      const float fix = scale_sum<S>(all[e], before - base);
 #pragma unroll
       for (int x = 0; x < 4; ++x) v[e][x] *= fix;
 #pragma unroll 2
       for (int k = 0; k < n; ++k) {
         const float* p = reinterpret_cast<const float*>(stage + k * bytes);
-        const float f = exp2_fast(p[h] - base);
+        float sum = p[S::kHeads + h];
+        const float f = scale_sum<S>(sum, p[h] - base);
         const float4 x = *reinterpret_cast<const float4*>(p + 2 * S::kHeads + h * S::kDim + d);
-        all[e] = fmaf(p[S::kHeads + h], f, all[e]);
+        all[e] += sum;
         v[e][0] = fmaf(x.x, f, v[e][0]);
         v[e][1] = fmaf(x.y, f, v[e][1]);
         v[e][2] = fmaf(x.z, f, v[e][2]);
@@ -1166,9 +1184,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float top = -INFINITY, all = 0.0f, v[4] = {};
         auto top_of = [&](int w) { top = fmaxf(top, ctl->m[w][h]); };
         auto add = [&](int w, float base) {
-          const float f = exp2_fast(ctl->m[w][h] - base);
+          float sum = ctl->sum[w][h];
+          const float f = scale_sum<S>(sum, ctl->m[w][h] - base);
           const float4 x = *reinterpret_cast<const float4*>(join + w * S::kJoinWarp + h * S::kJoinRow + d);
-          all = fmaf(ctl->sum[w][h], f, all);
+          all += sum;
           v[0] = fmaf(x.x, f, v[0]);
           v[1] = fmaf(x.y, f, v[1]);
           v[2] = fmaf(x.z, f, v[2]);
