@@ -100,14 +100,27 @@ def build(n_layers: int, batch: int, context: int, heads=16, kv_heads=4, dim=128
     return Decoder(blocks, heads, kv_heads, dim, batch, table)
 
 
-def main():
+SPARE = 8  # positions kept for the warm-up steps
+
+
+def arguments(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--batch", type=int, default=64)
     ap.add_argument("--context", type=int, default=4096)
     ap.add_argument("--layers", type=int, default=5)
     ap.add_argument("--steps", type=int, default=50)
     ap.add_argument("--cache", choices=("bf16", "e4m3"), default="e4m3")
-    args = ap.parse_args()
+    args = ap.parse_args(argv)
+    for name in ("batch", "layers", "steps"):
+        if getattr(args, name) < 1:
+            ap.error(f"--{name} must be 1 at least")
+    if args.context <= args.steps + SPARE:  # every timed step attends to a context, and stays in its pages
+        ap.error(f"--context must be above --steps + {SPARE} ({args.steps + SPARE})")
+    return args
+
+
+def main():
+    args = arguments()
     dec = build(args.layers, args.batch, args.context, cache_dtype=MOE_E4M3 if args.cache == "e4m3" else MOE_BF16)
     for b in dec.blocks:  # a context as if it had been decoded: random keys and values of every position
         g = torch.Generator(device="cuda").manual_seed(7)
@@ -116,7 +129,7 @@ def main():
             kv = torch.randn(args.context, 2 * dec.kv_heads, dec.dim, generator=g, device="cuda").bfloat16()
             moe.kv_write(kv[:, :dec.kv_heads], kv[:, dec.kv_heads:], b.cache, pos, dec.page_table, dec.attn_ws,
                          seq=torch.full_like(pos, s))
-    start = args.context - args.steps - 8
+    start = args.context - args.steps - SPARE
     embed = torch.randn_like(dec.residual)
 
     def rewind():
