@@ -279,7 +279,8 @@ typedef struct {
  * bf16 cache: values rounded to nearest even.  E4M3 cache: a row's exponent is the smallest power
  * of two (2^-127 at least) that brings its largest magnitude to 448 at most, and its codes are the
  * scaled values rounded to nearest even: scaling by a power of two is exact, so each value is
- * rounded once and moe_kv_read returns it without another rounding.
+ * rounded once and moe_kv_read returns it without another rounding.  A NaN stays one; an infinity is
+ * stored as 448 times 2^120, beyond fp32, reads back as an infinity, and sets its row's exponent.
  * A sequence outside [0, n_seqs), a position past the page table or a page outside [0, n_pages)
  * writes nothing and records MOE_ERR_BAD_PAGE in ws (any workspace of this library). */
 moe_status moe_kv_write(const moe_kv_cache* cache, const void* k, const void* v, moe_dtype kv_dtype, int64_t k_stride,
@@ -316,6 +317,11 @@ moe_status moe_attn_workspace_init(void* ws, size_t ws_bytes, moe_stream_t strea
  * outside [0, n_pages) is left out as if masked; both record MOE_ERR_BAD_PAGE.  What lies in the
  * cache outside the window (NaN and infinity included) has no effect.  Scores, sums and the
  * accumulators are fp32; the results do not depend on the order in which CTAs finish.
+ * Weights p_j are rounded before they multiply the values, and unrounded in the sum: to bf16 (off by
+ * 2^-8 of themselves at most) over a bf16 cache; as closely over an E4M3 cache, where those below 2^-75
+ * of the largest among 32 tokens lose bits.  Over an E4M3 cache query elements below 2^-14 of their
+ * head's largest are held to 2^-22 of that one.  So before its own rounding to bf16 an output is off by
+ * up to 2^-8 of sum_j p_j |v_j| / sum_j p_j.
  * n_heads a multiple of n_kv_heads, up to 1024; B up to 65536; max_pages * page_size up to 2^28, and
  * (max_pages * page_size / 32 + 1) * B * n_kv_heads * ceil(n_heads / n_kv_heads / 4) below 2^31. */
 moe_status moe_attn_decode(const moe_kv_cache* cache, const void* q, int64_t q_stride, int n_heads, int B,

@@ -550,9 +550,11 @@ struct WarpBf16 {
 // to the accumulator by an fp32 factor: a long row of small weights keeps its precision beside a large
 // one.  The split holds the 2^-8 down to 2^-15 of that maximum; where weights are smaller (and not 0),
 // they take a product of their own, 2^15 times as large, and so on, down to 2^-75 of it.  (They matter
-// where the large weights meet values of 0.)  With one product for all weights of a tile 64 sequences of
-// up to 8k tokens, groups of 8, took 68.9 us, like this 79.2.  The products are a loop, not copies: see
-// above on the size of the code (d 256: 77 us against 68).
+// where the large weights meet values of 0.)  So the time depends on how far apart the scores are.  With
+// one product for all weights of a tile 64 sequences of up to 8k tokens, groups of 8, took 68.9 us; like
+// this 71 at scores of a standard deviation of 1 nat, 79 at 1.7, 97 at 3, 122 at 5 and 156 at 9 (groups of
+// 4: 61, 62, 68, 82 and 104).  The products are a loop, not copies: see above on the size of the code
+// (52 mixed lengths of up to 499 tokens, 256 wide: 77 us against 68).
 //
 // The values' codes: a register of ldmatrix with transpose holds elements 2g and 2g + 1 of tokens 2t
 // and 2t + 1; a byte permutation of it and the one of tokens 2t + 8 and 2t + 9 gives the four
