@@ -58,8 +58,10 @@ typedef enum {
   MOE_ERR_CUDA = -6,          /* a CUDA runtime call failed */
   MOE_ERR_INDEX = -7,         /* MOE_DEBUG builds only: a kernel's index check failed (an internal
                                  error of the library; the access was kept inside its buffer) */
-  MOE_ERR_BAD_PAGE = -8       /* a token's sequence, position or page was outside the page table or
+  MOE_ERR_BAD_PAGE = -8,      /* a token's sequence, position or page was outside the page table or
                                  the cache */
+  MOE_ERR_NO_PAGES = -9       /* a sequence's new tokens did not fit: the pool had too few free pages, or
+                                 its row of the page table or the token list no room */
 } moe_status;
 
 /* MOE_E2M1: 4-bit weights (OCP E2M1 codes: sign bit 3, magnitudes 0, 0.5, 1, 1.5, 2, 3, 4,
@@ -68,7 +70,8 @@ typedef enum {
  * Kolibri Benchmark Before Scoring One Answer", section "What this means if you want Kolibri
  * on a Mac"; the pages give no format).  Weight matrices keep their row count and halve their
  * bytes per row; activations enter the contractions as E4M3 as for MOE_E4M3 (W4A8). */
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_E2M1 = 3 } moe_dtype;
+/* MOE_INT4: rows of a key-value cache in 4 bits (moe_kv_cache below), not a type of weights. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_E2M1 = 3, MOE_INT4 = 4 } moe_dtype;
 
 /* Byte order of the E4M3 expert weight tensors (w_gate_up, w_down, sh_gate_up, sh_down).
  *   MOE_LAYOUT_ROWS   the shapes below, row-major (a checkpoint's order).
@@ -252,14 +255,23 @@ moe_status moe_route_noalloc(const void* x, moe_dtype x_dtype, int T, const moe_
 
 /* A paged key-value cache: n_pages pages of page_size tokens, each token with n_kv_heads keys and
  * values of head_dim elements.
- *   k, v          [n_pages, n_kv_heads, page_size, head_dim]  bf16, or E4M3 codes
- *   k_exp, v_exp  [n_pages, n_kv_heads, page_size] uint8 (E4M3 only, else NULL): a row's values
- *                 are its codes times 2^(exp - 127)
+ *   k, v          [n_pages, n_kv_heads, page_size, head_dim]  bf16, or E4M3 codes; 4-bit codes
+ *                 (MOE_INT4): [.., head_dim / 2] bytes
+ *   k_exp, v_exp  [n_pages, n_kv_heads, page_size] uint8 (E4M3 and INT4, else NULL): a row's values
+ *                 are its codes (INT4: times their scales) times 2^(exp - 127)
+ *   k_scale, v_scale  [n_pages, n_kv_heads, page_size, 4 ceil(head_dim / 64)] uint8 (INT4 only, else not
+ *                 read): byte b of each 16 elements is their scale (1 + (b % 8) / 8) 2^(b / 8 - 12), from
+ *                 2^-12 to 15; the bytes past head_dim / 16 are zeros
+ * INT4: element i is n_i scale(i / 16) 2^(exp - 127) with n_i a whole number from -7 to 7.  Elements 4u ..
+ * 4u + 3 are bytes 2u and 2u + 1 of their row: the codes n_i + 8, the first in the lowest four bits of
+ * 16, and those 16 bits turned left by 3 (the order that attention takes apart in the fewest steps).  A row is
+ * 0.57 bytes an element, against 1.01 in E4M3 and 2 in bf16.
  * Position p of sequence s lives in row p % page_size of page page_table[s, p / page_size], of a
  * page_table [n_seqs, max_pages] int32 on the device that the caller fills as it hands out pages
  * (entries beyond a sequence's length are not read).
- * dtype MOE_BF16 or MOE_E4M3; page_size a multiple of 16, up to 4096; head_dim a multiple of 16, up
- * to 256; n_kv_heads up to 1024; n_pages * n_kv_heads * page_size below 2^31; all pointers 16-byte aligned. */
+ * dtype MOE_BF16, MOE_E4M3 or MOE_INT4; page_size a multiple of 16, up to 4096; head_dim a multiple of 16
+ * (INT4: of 32), up to 256; n_kv_heads up to 1024; n_pages * n_kv_heads * page_size below 2^31; all pointers
+ * 16-byte aligned.  (k_scale and v_scale are looked at for MOE_INT4 alone.) */
 typedef struct {
   int n_pages, page_size, n_kv_heads, head_dim;
   moe_dtype dtype;
@@ -267,6 +279,8 @@ typedef struct {
   void* v;
   uint8_t* k_exp;
   uint8_t* v_exp;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
 } moe_kv_cache;
 
 /* Writes T tokens' keys and values into the cache.
@@ -281,6 +295,11 @@ typedef struct {
  * scaled values rounded to nearest even: scaling by a power of two is exact, so each value is
  * rounded once and moe_kv_read returns it without another rounding.  A NaN stays one; an infinity is
  * stored as 448 times 2^120, beyond fp32, reads back as an infinity, and sets its row's exponent.
+ * INT4 cache: a row's exponent is the smallest power of two, from 2^-111 to 2^119, that brings its largest
+ * magnitude to 105 at most; then the scale of 16 elements is the smallest that brings theirs to 7 at most; then
+ * each element is rounded once, to the nearest of -7 .. 7, ties to the even one.  So it is off by at most half its
+ * group's scale; magnitudes above 105 times 2^119 become that.  A row with an infinity or a NaN in it reads back
+ * as NaN (exponent byte 255).
  * A sequence outside [0, n_seqs), a position past the page table or a page outside [0, n_pages)
  * writes nothing and records MOE_ERR_BAD_PAGE in ws (any workspace of this library). */
 moe_status moe_kv_write(const moe_kv_cache* cache, const void* k, const void* v, moe_dtype kv_dtype, int64_t k_stride,
@@ -321,12 +340,121 @@ moe_status moe_attn_workspace_init(void* ws, size_t ws_bytes, moe_stream_t strea
  * 2^-8 of themselves at most) over a bf16 cache; as closely over an E4M3 cache, where those below 2^-75
  * of the largest among 32 tokens lose bits.  Over an E4M3 cache query elements below 2^-14 of their
  * head's largest are held to 2^-22 of that one.  So before its own rounding to bf16 an output is off by
- * up to 2^-8 of sum_j p_j |v_j| / sum_j p_j.
+ * up to 2^-8 of sum_j p_j |v_j| / sum_j p_j.  An INT4 cache's values are exact in bf16, and attention over it is
+ * that over a bf16 cache of the same values.  A weight below 2^-126 of the row's largest is 0.
  * n_heads a multiple of n_kv_heads, up to 1024; B up to 65536; max_pages * page_size up to 2^28, and
  * (max_pages * page_size / 32 + 1) * B * n_kv_heads * ceil(n_heads / n_kv_heads / 4) below 2^31. */
 moe_status moe_attn_decode(const moe_kv_cache* cache, const void* q, int64_t q_stride, int n_heads, int B,
                            const int32_t* lens, const int32_t* page_table, int max_pages, float scale, int window,
                            void* out, float* lse, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---- the pages and places of new tokens ----------------------------------------------------------
+ *
+ * A serving step knows how many tokens each sequence has in the cache and how many it gets.  The calls
+ * below keep the page table, the pool of free pages and the lengths on the device, so that a step that
+ * a CUDA graph replays hands out pages by itself.
+ *   lens        [B] int32: tokens that each sequence has in the cache (a negative one counts as 0)
+ *   page_table  [B, max_pages] int32 as above; a sequence holds the first ceil(len / page_size) entries, and no
+ *               page belongs to two sequences
+ *   free_pages  [n_pages] int32: a stack, whose first n_free[0] entries are the free pages
+ * Both calls are given the workspace of moe_pages_workspace_bytes and report to its status record. */
+size_t moe_pages_workspace_bytes(int B);
+
+/* Room for new tokens.
+ *   new_tokens  [B] int32: tokens to come for each sequence (negative: 0); NULL: one each
+ *   lens_out    [B], n_free_out [1]: the lengths and the count of free pages afterwards (may be lens and
+ *               n_free themselves)
+ *   starts      [B + 1] int32: where each sequence's tokens begin on the list of all new tokens (in the order of
+ *               sequences), cut to max_tokens
+ *   seq, pos, slot  [max_tokens] int32: each new token's sequence and position, and its place in the cache,
+ *               page * page_size + row; -1 in all three behind the last token
+ * A sequence that needs pages takes them from the top of the stack, sequences in order, and its entries of the
+ * page table are written.  A sequence gets nothing if its tokens would go past its row of the page table or past
+ * max_tokens, or if it needs pages and those of the sequences before it (served or not for want of pages) leave too
+ * few: its tokens keep their place on the list with pos and slot -1 (moe_kv_write and moe_rope_kv_write skip those), its
+ * length stays, and MOE_ERR_NO_PAGES is recorded.  A page outside [0, n_pages) in the table or in the pool gives
+ * slots of -1, and an n_free outside [0, n_pages] counts as the nearest; both record MOE_ERR_BAD_PAGE.
+ * B up to 65536, max_tokens up to 2^20, page_size 1 to 4096, max_pages * page_size up to 2^28, n_pages *
+ * page_size below 2^31; lens_out, n_free_out, starts, seq, pos, slot apart from each other and from every input but
+ * as above. */
+moe_status moe_page_plan(const int32_t* lens, const int32_t* new_tokens, int B, int32_t* page_table, int max_pages,
+                         const int32_t* free_pages, const int32_t* n_free, int n_pages, int page_size, int max_tokens,
+                         int32_t* lens_out, int32_t* n_free_out, int32_t* starts, int32_t* seq, int32_t* pos,
+                         int32_t* slot, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The pages of ended sequences back to the pool: each sequence with ended[b] != 0 ([B] bytes) puts its pages on
+ * the stack, sequences in order, and has length 0 afterwards; the page table stays as it is.  Lengths past the page table
+ * are cut to it, and pages that the stack of n_pages entries has no room for are dropped; both record
+ * MOE_ERR_BAD_PAGE.  lens_out and n_free_out as above. */
+moe_status moe_page_release(const int32_t* lens, const uint8_t* ended, int B, const int32_t* page_table, int max_pages,
+                            int32_t* free_pages, const int32_t* n_free, int n_pages, int page_size, int32_t* lens_out,
+                            int32_t* n_free_out, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---- rotary positions ------------------------------------------------------------------------------
+ *
+ * The first `dim` elements of a head are pairs, each turned by an angle that grows with the token's position p:
+ *   (a, b) -> m (a cos t - b sin t, b cos t + a sin t),   t = p f_i,   i = 0 .. dim / 2 - 1
+ * with pair i the elements i and i + dim / 2, or 2i and 2i + 1 (interleaved); elements from dim on stay.
+ *   turns      [dim / 2] uint64 on the device: f_i as a fraction of a turn in units of 2^-64.  p times that, modulo
+ *              2^64, is the angle however far the position is, without 64-bit floating point (kernels take it to
+ *              fp32 with an error below 2^-27 of a turn)
+ *   magnitude  m, which some of the ways to stretch a context come with */
+typedef struct {
+  int dim, interleaved;
+  float magnitude;
+  const uint64_t* turns;
+} moe_rope_table;
+
+/* The frequencies f_i = base^(-2i / dim), as trained for a context of `original` positions, or changed for one
+ * `factor` times as long:
+ *   MOE_ROPE_LINEAR    f_i / factor (positions moved closer together)
+ *   MOE_ROPE_BASE      base * factor^(dim / (dim - 2)) in place of base (dim > 2)
+ *   MOE_ROPE_BY_INDEX  f_i (1 - r_i) + f_i / factor r_i with r_i = clamp((i - i0) / max(i1 - i0, 0.001), 0, 1):
+ *                      pairs that turn more than `high` times in the original context stay, those below `low`
+ *                      turns are slowed; i(x) = dim ln(original / (2 pi x)) / (2 ln base) is the index of x turns,
+ *                      i0 = max(floor(i(high)), 0), i1 = min(ceil(i(low)), dim - 1); magnitude 0.1 ln factor + 1
+ *   MOE_ROPE_BY_TURNS  the same blend with 1 - r_i = clamp((x_i - low) / (high - low), 0, 1), x_i = original f_i /
+ *                      (2 pi) the pair's turns in the original context; magnitude 1 */
+typedef enum {
+  MOE_ROPE_PLAIN = 0,
+  MOE_ROPE_LINEAR = 1,
+  MOE_ROPE_BASE = 2,
+  MOE_ROPE_BY_INDEX = 3,
+  MOE_ROPE_BY_TURNS = 4
+} moe_rope_scaling;
+
+/* turns_out [dim / 2] and magnitude_out [1] of those frequencies (host memory; a host computation in 64 bits).
+ * dim even, 2 to 256; base > 1; factor >= 1; original, low and high above 0 and low < high where they are used. */
+moe_status moe_rope_frequencies(int dim, double base, moe_rope_scaling scaling, double factor, double original, double low,
+                                double high, uint64_t* turns_out, float* magnitude_out);
+
+/* turns_out [n] of frequencies [n] in radians a position (host memory), for any other rule.  Finite, of magnitude
+ * below 2^31. */
+moe_status moe_rope_turns(const double* frequencies, int n, uint64_t* turns_out);
+
+/* x turned: rows of [n_heads, head_dim] bf16 or fp32 (dtype), x_stride elements apart, to out, likewise with
+ * out_stride (out may be x, with its stride; else apart from it).  pos [T] int32, any value; inverse != 0 turns back
+ * (with the same magnitude): the gradient of the operator, and, with it, positions moved by a difference.
+ * Products and sums are fp32, rounded once.  head_dim a multiple of 8, up to 256; rope->dim a multiple of 8, up to
+ * head_dim; n_heads up to 1024; strides a multiple of 16 bytes; x and out 16-byte aligned. */
+moe_status moe_rope_apply(const moe_rope_table* rope, const void* x, int64_t x_stride, void* out, int64_t out_stride,
+                          moe_dtype dtype, int T, int n_heads, int head_dim, const int32_t* pos, int inverse,
+                          moe_stream_t stream);
+
+/* A step's queries and keys turned, and keys and values into the cache, in one launch.
+ *   q       rows of [n_heads, head_dim], k, v rows of [n_kv_heads, head_dim], bf16 or fp32 (dtype), q_stride,
+ *           k_stride and v_stride elements apart (multiples of 16 bytes)
+ *   q_out   bf16 rows of [n_heads, head_dim], q_out_stride elements apart: what moe_attn_decode takes (may be q, with its
+ *           stride, where that is bf16; else apart from it)
+ *   pos     [T] int32: for the angles (a negative one too)
+ *   slot    [T] int32: page * page_size + row of each token's place (moe_page_plan); negative: the key and value are
+ *           not written.  A slot past the cache writes nothing and records MOE_ERR_BAD_PAGE in ws.  Two tokens of one call
+ *           must not be given one place.
+ * Keys are rounded, or quantised as by moe_kv_write, once, from their turned fp32 values. */
+moe_status moe_rope_kv_write(const moe_rope_table* rope, const moe_kv_cache* cache, const void* q, int64_t q_stride,
+                             int n_heads, void* q_out, int64_t q_out_stride, const void* k, const void* v,
+                             moe_dtype dtype, int64_t k_stride, int64_t v_stride, int T, const int32_t* pos,
+                             const int32_t* slot, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* What stands between two blocks on the residual stream, in one pass over [T, d]:
  *   z  = y * rsqrt(mean(y^2) + eps) * w_post     (w_post NULL: z = y)

@@ -15,20 +15,21 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
-MOE_F32, MOE_BF16, MOE_E4M3, MOE_E2M1 = 0, 1, 2, 3
+MOE_F32, MOE_BF16, MOE_E4M3, MOE_E2M1, MOE_INT4 = 0, 1, 2, 3, 4
 LAYOUT_ROWS, LAYOUT_TILED = 0, 1
 BIAS_SCORE, BIAS_SELECT = 0, 1
 PATH_AUTO, PATH_STREAM, PATH_TC = 0, 1, 2
 STATUS = {0: "MOE_OK", -1: "MOE_ERR_INVALID_ARG", -2: "MOE_ERR_UNSUPPORTED", -3: "MOE_ERR_WORKSPACE",
           -4: "MOE_ERR_BAD_FORCED_ID", -5: "MOE_ERR_TIMEOUT", -6: "MOE_ERR_CUDA", -7: "MOE_ERR_INDEX",
-          -8: "MOE_ERR_BAD_PAGE"}
+          -8: "MOE_ERR_BAD_PAGE", -9: "MOE_ERR_NO_PAGES"}
 
 # every entry point include/libmoe.h declares
 EXPORTS = ("moe_workspace_bytes", "moe_workspace_init", "moe_route", "moe_dispatch", "moe_forward",
            "moe_forward_stack", "moe_forward_traced", "moe_forward_stack_traced", "moe_get_status",
            "moe_status_string", "moe_e4m3_encode", "moe_route_noalloc", "moe_selftest_wait_timeout",
            "moe_pack_weights", "moe_kv_write", "moe_kv_read", "moe_attn_workspace_bytes", "moe_attn_workspace_init",
-           "moe_attn_decode", "moe_block_norm")
+           "moe_attn_decode", "moe_block_norm", "moe_pages_workspace_bytes", "moe_page_plan", "moe_page_release",
+           "moe_rope_frequencies", "moe_rope_turns", "moe_rope_apply", "moe_rope_kv_write")
 TRACE_POINTS = 9
 TRACE_STAGES = ("router", "select", "dispatch", "act_quant", "gate_up", "h_quant", "down", "combine")
 
@@ -100,10 +101,20 @@ def load(path: str):
     L.moe_attn_workspace_init.argtypes = [vp, sz, vp]
     L.moe_attn_decode.argtypes = [vp, vp, i64, i32, i32, vp, vp, i32, f32, i32, vp, vp, vp, sz, vp]
     L.moe_block_norm.argtypes = [vp, i32, vp, vp, i32, i64, f32, vp, vp, i32, vp, vp, i32, i32, i32, f32, vp]
+    f64 = ctypes.c_double
+    L.moe_pages_workspace_bytes.argtypes = [i32]
+    L.moe_pages_workspace_bytes.restype = sz
+    L.moe_page_plan.argtypes = [vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_page_release.argtypes = [vp, vp, i32, vp, i32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+    L.moe_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp, vp]
+    L.moe_rope_turns.argtypes = [vp, i32, vp]
+    L.moe_rope_apply.argtypes = [vp, vp, i64, vp, i64, i32, i32, i32, i32, vp, i32, vp]
+    L.moe_rope_kv_write.argtypes = [vp, vp, vp, i64, i32, vp, i64, vp, vp, i32, i64, i64, i32, vp, vp, vp, sz, vp]
     for f in ("moe_workspace_init", "moe_route", "moe_dispatch", "moe_forward", "moe_forward_stack",
               "moe_forward_traced", "moe_forward_stack_traced", "moe_get_status", "moe_e4m3_encode",
               "moe_route_noalloc", "moe_selftest_wait_timeout", "moe_pack_weights", "moe_kv_write", "moe_kv_read",
-              "moe_attn_workspace_init", "moe_attn_decode", "moe_block_norm"):
+              "moe_attn_workspace_init", "moe_attn_decode", "moe_block_norm", "moe_page_plan", "moe_page_release",
+              "moe_rope_frequencies", "moe_rope_turns", "moe_rope_apply", "moe_rope_kv_write"):
         getattr(L, f).restype = i32
     return L
 

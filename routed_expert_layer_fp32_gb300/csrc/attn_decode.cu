@@ -81,23 +81,26 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinExp = -100;  // least value exponent that enters m: keeps the sum inside fp32's range
 static_assert(kMaxCtas <= kAttnTickets, "a counter a CTA");
 
-template <bool kE4M3_, int kDim_, int kHeads_>
+template <RowKind kRows_, int kDim_, int kHeads_>
 struct Shape {
-  static constexpr bool kE4M3 = kE4M3_;
+  static constexpr RowKind kRows = kRows_;
+  static constexpr bool kE4M3 = kRows == RowKind::kE4M3, kInt4 = kRows == RowKind::kInt4;
   static constexpr int kDim = kDim_;      // head_dim rounded up to 64, 128 or 256 (copies fill with zeros)
   static constexpr int kHeads = kHeads_;  // query heads of a segment
-  static constexpr int kRow = kDim * (kE4M3 ? 1 : 2);       // bytes
+  static constexpr int kRow = kE4M3 ? kDim : kInt4 ? kDim / 2 : kDim * 2;  // bytes
   static constexpr int kSpan = kRow < 128 ? kRow : 128;     // bytes of a row in one swizzled copy
   static constexpr int kSpans = kRow / kSpan;
   static constexpr int kSpanElems = kDim / kSpans;
   // 32 KB stages (16 KB for the narrowest rows); 16 or 32 tokens a warp, those of one product with the
   // values
-  static constexpr int kPerWarp = kE4M3 ? 32 : 16;
+  static constexpr int kPerWarp = kE4M3 || kInt4 ? 32 : 16;
   static constexpr int kTokens = kRow <= 128 ? 128 : 128 * 128 / kRow;
   static constexpr int kGroupWarps = kTokens / kPerWarp;
   static constexpr int kGroups = kWarps / kGroupWarps;
   static constexpr int kTile = kTokens * kRow;
-  static constexpr int kExps = kE4M3 ? 2 * kTokens : 0;     // the keys' and the values' exponents
+  static constexpr int kScales = kInt4 ? kTokens * (kDim / 16) : 0;  // room for the keys', or the values', scales
+  // the keys' and the values' exponents, then their scales
+  static constexpr int kExps = kE4M3 || kInt4 ? 2 * kTokens + 2 * kScales : 0;
   static constexpr int kStage = 2 * kTile;
   // the queries of kSlots segments as B operands: kQueryRegs registers a lane, and a factor a head
   static constexpr int kQueryRegs = kE4M3 ? kDim / 32 * (kHeads / 4) * 2 : kDim / 16 * (kHeads / 8) * 2;
@@ -123,7 +126,8 @@ struct Shape {
   static constexpr size_t kFixed = size_t(kSlots) * kQueries + size_t(kWarps) * kJoinWarp * 4 + sizeof(Control) + 1024;
   static constexpr int kRoom = int((kSmemLimit - kFixed) / (kStage + kExps));
   // a multiple of the groups: each has as many stages as the others
-  static constexpr int kStages = (kRoom < 192 * 1024 / kStage ? kRoom : 192 * 1024 / kStage) / kGroups * kGroups;
+  static constexpr int kWanted = 192 * 1024 / kStage < kMaxStages ? 192 * 1024 / kStage : kMaxStages;
+  static constexpr int kStages = (kRoom < kWanted ? kRoom : kWanted) / kGroups * kGroups;
   static constexpr size_t kExpsAt = size_t(kStages) * kStage;
   static constexpr size_t kQueriesAt = kExpsAt + size_t(kStages) * kExps;
   static constexpr size_t kJoinAt = kQueriesAt + size_t(kSlots) * kQueries;
@@ -323,9 +327,10 @@ struct Parts {
 
 // What a consumer warp needs to know of a tile.
 struct TileView {
-  uint32_t k, v;        // shared-memory addresses of the key and value tiles
-  const uint8_t* exps;  // of the keys; the values' follow kTokens further
-  uint32_t seen;        // a bit for each of the warp's tokens
+  uint32_t k, v;          // shared-memory addresses of the key and value tiles
+  const uint8_t* exps;    // of the keys; the values' follow kTokens further
+  const uint8_t* scales;  // of the keys; the values' follow kScales further
+  uint32_t seen;          // a bit for each of the warp's tokens
 };
 
 // Addresses for ldmatrix.  A tile lies in shared memory box by box (the tokens of one copy, a multiple
@@ -368,29 +373,27 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int row0, int box, uin
   }
 }
 
-// One warp's running result over a bf16 cache.  Scores: keys (16 tokens x 16 elements, as they lie)
-// times queries; the weights, rounded to bf16 (the type of the values: a product's operands have
-// one), go through an 8 x 8 transpose to become the B operand of values^T times weights.  Lane
-// (g, t) = (lane / 4, lane % 4) holds tokens g and g + 8 of a block, and heads 2t and 2t + 1 of a
-// block of eight.
+// INT4: the values of the rows that a warp does not see made zeros by their scales and exponents (a lane a row).
 template <typename S>
-struct WarpBf16 {
-  static constexpr int kMT = S::kPerWarp / 16, kKS = S::kDim / 16, kNB = S::kHeads / 8;
-  uint32_t q[kKS][kNB][2];
-  float m[kNB][2], sum[kNB][2], acc[kKS][kNB][4];
-  float factor;  // scores to base-2 exponents
-  Rows<S> k_rows, v_rows;
-  int g, t;
+__device__ __forceinline__ void clear_scales(uint8_t* exps, int pitch, int row0, uint32_t seen, int lane) {
+  static_assert(!S::kInt4 || S::kPerWarp == 32, "a lane a row");
+  if (seen >> lane & 1) return;
+  exps[S::kTokens + lane] = 15;
+  uint32_t* s = reinterpret_cast<uint32_t*>(exps - row0 + 2 * S::kTokens + S::kScales + (row0 + lane) * pitch);
+  for (int w = 0; w < pitch / 4; ++w) s[w] = 0u;
+}
 
-  __device__ __forceinline__ WarpBf16(int row0, int lane, int box)
-      : k_rows(row0 + (lane & 15), lane >> 4, box),
-        v_rows(row0 + (lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1, box),
-        g(lane >> 2),
-        t(lane & 3) {}
+// A bf16 cache's operands: rows as they lie.
+template <typename S>
+struct Bf16Operands {
+  static constexpr int kKS = S::kDim / 16, kNB = S::kHeads / 8;
+  Rows<S> k_rows, v_rows;
+
+  __device__ __forceinline__ Bf16Operands(int row0, int lane, int box, int)
+      : k_rows(row0 + (lane & 15), lane >> 4, box), v_rows(row0 + (lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1, box) {}
 
   // Register [ks][nb][i] of lane (g, t): head nb * 8 + g, elements 16 ks + 8 i + 2t and the next.
-  static __device__ __forceinline__ void lay_out(uint8_t* queries, const __nv_bfloat16* q, int heads, int dim,
-                                                 float scale_log2e, int lane) {
+  static __device__ __forceinline__ void lay_out(uint8_t* queries, const __nv_bfloat16* q, int heads, int dim, int lane) {
     const int g = lane >> 2, t = lane & 3;
     uint32_t r[kNB][kKS][2];
 #pragma unroll
@@ -408,6 +411,222 @@ struct WarpBf16 {
       for (int ks = 0; ks < kKS; ks += 2)
         *reinterpret_cast<uint4*>(queries + ((nb * kKS + ks) / 2 * 32 + lane) * 16) =
             make_uint4(r[nb][ks][0], r[nb][ks][1], r[nb][ks + 1][0], r[nb][ks + 1][1]);
+  }
+
+  __device__ __forceinline__ void key(const TileView& tv, int mt, int ks, uint32_t (&r)[4]) {
+    ldmatrix4(k_rows(tv.k, mt, ks), r);
+  }
+  __device__ __forceinline__ void value(const TileView& tv, int mt, int ks, uint32_t (&r)[4]) {
+    ldmatrix4_trans(v_rows(tv.v, mt, ks), r);
+  }
+  // Elements of head h, `j0` products of 16 elements on, out of the accumulators of kPassDim / 16 of them.
+  template <typename Acc>
+  static __device__ __forceinline__ void put(float* out, const Acc& acc, int j0, int nb, int i, int lane) {
+#pragma unroll
+    for (int j = 0; j < S::kPassDim / 16; ++j) {
+      out[j * 16 + (lane >> 2)] = acc[j0 + j][nb][i];
+      out[j * 16 + 8 + (lane >> 2)] = acc[j0 + j][nb][2 + i];
+    }
+  }
+};
+
+// An INT4 cache's operands: bf16 numbers made of the codes, n s 2^e exactly, so that all that follows is as over a bf16
+// cache of these values.
+//
+// A code c = n + 8 of four bits at mantissa bits 3 to 6 of a bf16 number 128 makes it 128 + 8c = 192 + 8n: one AND and
+// OR for two codes, one in each half of a register, after a shift that the cache's order of bits makes unnecessary for
+// two of eight.  One fused multiply-add with (u, -192 u), u = s 2^e / 8, gives 8n u = n s 2^e without rounding.  u's bits
+// are the scale's byte, moved to where its three mantissa bits belong, plus the exponents (E + e - 15, all biased).  So
+// eight codes take 15 instructions, 11 of them to take the codes apart.
+//
+// Keys.  The products' element axis may be in any order that queries share: lane (g, t) reads a quarter t of rows g
+// and g + 8 in whole words, so that a word is two products' operands and a lane needs the scales of its own quarter only.
+// Values.  ldmatrix with transpose moves 16-bit units: four elements of one token.  Lane (g, t) gets unit g of a 16-byte
+// chunk for tokens 2t and 2t + 1: a pair of codes is one element of two tokens, as the A operand of values^T takes it;
+// rows g and g + 8 of a product are two elements of a unit.
+//
+// Rows that a warp does not see have their values' scales and exponents set to what makes u = 0, whatever the codes are.
+// An exponent byte of 255 makes u an infinity or a NaN, and the values inf - inf.
+constexpr uint32_t kInt4Zero = 15;  // the exponent byte that makes u = 0 of scale byte 0
+
+template <typename S>
+struct Int4Operands {
+  static constexpr int kKS = S::kDim / 16, kNB = S::kHeads / 8;
+  static constexpr int kWords = S::kDim / 32;       // of a lane's quarter of a row, eight codes each
+  static constexpr int kPitchWords = S::kDim / 64;  // of a row's scales
+  uint32_t k_at, k_flip, v_at, v_flip;  // rows and swizzle of the lane's key words and ldmatrix rows
+  int pitch, k_col, g, t;
+  uint32_t pick[2];                     // byte selectors for the scales of two tokens
+  uint32_t word[2][kWords], unit[2][kWords / 2], minus[2][kWords / 2];  // key rows g and g + 8
+  uint32_t chunk[4], v_scale[4][kPitchWords], v_exp[2];
+
+  // 16-byte chunk i of row r lies at chunk i ^ flip(r)
+  static __device__ __forceinline__ uint32_t swizzle(int r) {
+    return S::kRow == 32 ? (r >> 2) & 1 : S::kRow == 64 ? (r >> 1) & 3 : r & 7;
+  }
+  __device__ __forceinline__ Int4Operands(int row0, int lane, int, int dim) : g(lane >> 2), t(lane & 3) {
+    k_at = uint32_t((row0 + g) * S::kRow);
+    k_flip = swizzle(row0 + g);  // rows 8 further have the same
+    const int v_row = row0 + (lane & 15);
+    v_at = uint32_t(v_row * S::kRow);
+    v_flip = swizzle(v_row) ^ (lane >> 4);
+    pitch = scale_pitch(dim);
+    // a quarter past the row's end holds no codes that count (the queries there are 0): any scale will do
+    const int col = t * (S::kDim / 64);
+    k_col = col * 16 < dim ? col : 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t k = 2 * i + (g >> 2);
+      pick[i] = k | (8 + k) << 4 | (4 + k) << 8 | (12 + k) << 12;  // 8 +: the byte's sign, 0 in every scale
+    }
+  }
+
+  // Register [ks][nb][i] of lane (g, t): head nb * 8 + g; word ks / 2 of the quarter, its elements 2 (ks % 2) + i and 4
+  // further.
+  static __device__ __forceinline__ void lay_out(uint8_t* queries, const __nv_bfloat16* q, int heads, int dim, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    uint4 u[kNB][kWords];
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        const int d = t * (S::kDim / 4) + w * 8;
+        u[nb][w] = nb * 8 + g < heads && d < dim
+                       ? __ldg(reinterpret_cast<const uint4*>(q + int64_t(nb * 8 + g) * dim + d))
+                       : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+    for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        const uint4 x = u[nb][w];
+        *reinterpret_cast<uint4*>(queries + ((nb * kKS + 2 * w) / 2 * 32 + lane) * 16) =
+            make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                       __byte_perm(x.y, x.w, 0x7632));
+      }
+  }
+
+  // __byte_perm, whose selectors know no signs
+  static __device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t scaled(uint32_t x, uint32_t u, uint32_t m) {
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&u),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&m));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static __device__ __forceinline__ uint32_t times_minus_192(uint32_t u) {
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), __float2bfloat162_rn(-192.0f));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  // Codes 2j and 2j + 1 of both halves, as 192 + 8n.
+  static __device__ __forceinline__ void codes(uint32_t w, int j, uint32_t& a, uint32_t& b) {
+    if (j == 1) w = __byte_perm(w, 0u, 0x2301);  // each half's bytes exchanged: turned by 8
+    a = (w & 0x00780078u) | 0x43004300u;
+    b = (w >> 4 & 0x00780078u) | 0x43004300u;
+  }
+
+  __device__ __forceinline__ void key(const TileView& tv, int mt, int ks, uint32_t (&r)[4]) {
+    if (ks == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = mt * 16 + h * 8;  // the swizzle is that of row g
+        const uint32_t at = tv.k + k_at + uint32_t(row * S::kRow);
+        if constexpr (S::kDim == 64) {
+          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                       : "=r"(word[h][0]), "=r"(word[h][1])
+                       : "r"(at + (((t >> 1) ^ k_flip) << 4) + (t & 1) * 8)
+                       : "memory");
+        } else {
+#pragma unroll
+          for (int i = 0; i < kWords / 4; ++i)
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(word[h][4 * i]), "=r"(word[h][4 * i + 1]), "=r"(word[h][4 * i + 2]), "=r"(word[h][4 * i + 3])
+                         : "r"(at + (((t * (kWords / 4) + i) ^ k_flip) << 4))
+                         : "memory");
+        }
+        const uint8_t* s = tv.scales + (row + g) * pitch + k_col;
+        uint32_t bytes;
+        if constexpr (S::kDim == 64) bytes = *s;
+        else if constexpr (S::kDim == 128) bytes = *reinterpret_cast<const uint16_t*>(s);
+        else bytes = *reinterpret_cast<const uint32_t*>(s);
+        const uint32_t e = (uint32_t(tv.exps[row + g]) - kInt4Zero) * 0x00800080u;
+#pragma unroll
+        for (int i = 0; i < kWords / 2; ++i) {
+          unit[h][i] = __byte_perm(bytes, 0u, 0x4040 + i * 0x0101) * 16u + e;
+          minus[h][i] = times_minus_192(unit[h][i]);
+        }
+      }
+    }
+    const int w = ks / 2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t a, b;
+      codes(word[h][w], ks & 1, a, b);
+      r[h] = scaled(a, unit[h][w / 2], minus[h][w / 2]);
+      r[2 + h] = scaled(b, unit[h][w / 2], minus[h][w / 2]);
+    }
+  }
+
+  // Product md: chunk md / 2 of 32 elements, elements 2 (md % 2) and the next of each unit of four.
+  __device__ __forceinline__ void value(const TileView& tv, int mt, int md, uint32_t (&r)[4]) {
+    if (md == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+        const uint8_t* s = tv.scales + S::kScales + (mt * 16 + 2 * t + (i & 1) + (i >> 1) * 8) * pitch;
+#pragma unroll
+        for (int w = 0; w < kPitchWords; ++w) v_scale[i][w] = reinterpret_cast<const uint32_t*>(s)[w];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t e = *reinterpret_cast<const uint16_t*>(tv.exps + S::kTokens + mt * 16 + 2 * t + i * 8);
+        v_exp[i] = __byte_perm(e, 0u, 0x4140) * 128u - kInt4Zero * 0x00800080u;
+      }
+    }
+    if (md % 4 == 0) ldmatrix4_trans(tv.v + v_at + uint32_t(mt * 16 * S::kRow) + (((md / 2) ^ v_flip) << 4), chunk);
+    const int c = md / 2, cc = c & 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // tokens 2t and 2t + 1, and 8 further
+      const uint32_t u = permute(v_scale[2 * i][c / 2], v_scale[2 * i + 1][c / 2], pick[cc]) * 16u + v_exp[i];
+      const uint32_t m = times_minus_192(u);
+      uint32_t a, b;
+      codes(chunk[2 * cc + i], md & 1, a, b);
+      r[2 * i] = scaled(a, u, m);
+      r[2 * i + 1] = scaled(b, u, m);
+    }
+  }
+  template <typename Acc>
+  static __device__ __forceinline__ void put(float* out, const Acc& acc, int j0, int nb, int i, int lane) {
+#pragma unroll
+    for (int j = 0; j < S::kPassDim / 16; j += 2)
+      *reinterpret_cast<float4*>(out + j * 16 + (lane >> 2) * 4) =
+          make_float4(acc[j0 + j][nb][i], acc[j0 + j][nb][2 + i], acc[j0 + j + 1][nb][i], acc[j0 + j + 1][nb][2 + i]);
+  }
+};
+
+// One warp's running result where the operands are bf16.  Scores: keys (16 tokens x 16 elements)
+// times queries; the weights, rounded to bf16 (the type of the values: a product's operands have
+// one), go through an 8 x 8 transpose to become the B operand of values^T times weights.  Lane
+// (g, t) = (lane / 4, lane % 4) holds tokens g and g + 8 of a block, and heads 2t and 2t + 1 of a
+// block of eight.
+template <typename S>
+struct WarpBf16 {
+  using Operands = std::conditional_t<S::kInt4, Int4Operands<S>, Bf16Operands<S>>;
+  static constexpr int kMT = S::kPerWarp / 16, kKS = S::kDim / 16, kNB = S::kHeads / 8;
+  uint32_t q[kKS][kNB][2];
+  float m[kNB][2], sum[kNB][2], acc[kKS][kNB][4];
+  float factor;  // scores to base-2 exponents
+  Operands operands;
+  int g, t;
+
+  __device__ __forceinline__ WarpBf16(int row0, int lane, int box, int dim)
+      : operands(row0, lane, box, dim), g(lane >> 2), t(lane & 3) {}
+
+  static __device__ __forceinline__ void lay_out(uint8_t* queries, const __nv_bfloat16* q, int heads, int dim,
+                                                 float scale_log2e, int lane) {
+    Operands::lay_out(queries, q, heads, dim, lane);
     if (lane < S::kHeads) reinterpret_cast<float*>(queries + S::kQueryRegs * 128)[lane] = scale_log2e;
   }
 
@@ -442,7 +661,7 @@ struct WarpBf16 {
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         uint32_t r[4];
-        ldmatrix4(k_rows(tv.k, mt, ks), r);
+        operands.key(tv, mt, ks, r);
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) mma_bf16_16x8x16(ks & 1 ? s2[nb] : s[mt][nb], r, q[ks][nb][0], q[ks][nb][1]);
       }
@@ -498,7 +717,7 @@ struct WarpBf16 {
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         uint32_t r[4];
-        ldmatrix4_trans(v_rows(tv.v, mt, ks), r);
+        operands.value(tv, mt, ks, r);
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) mma_bf16_16x8x16(acc[ks][nb], r, w[mt][nb][0], w[mt][nb][1]);
       }
@@ -526,11 +745,7 @@ struct WarpBf16 {
       for (int i = 0; i < 2; ++i) {
         const int h = nb * 8 + 2 * t + i;
         if (h >= heads) continue;  // columns without a head
-#pragma unroll
-        for (int j = 0; j < S::kPassDim / 16; ++j) {
-          out[h * S::kJoinRow + j * 16 + g] = acc[kPass * (S::kPassDim / 16) + j][nb][i];
-          out[h * S::kJoinRow + j * 16 + 8 + g] = acc[kPass * (S::kPassDim / 16) + j][nb][2 + i];
-        }
+        Operands::put(out + h * S::kJoinRow, acc, kPass * (S::kPassDim / 16), nb, i, g * 4 + t);
       }
   }
 };
@@ -579,7 +794,7 @@ struct WarpE4M3 {
   Rows<S> rows;
   int g, t;
 
-  __device__ __forceinline__ WarpE4M3(int row0, int lane, int box)
+  __device__ __forceinline__ WarpE4M3(int row0, int lane, int box, int)
       : rows(row0 + (lane & 15), lane >> 4, box), g(lane >> 2), t(lane & 3) {}
 
   // The hi (x) and lo (y) codes of four query elements.
@@ -919,8 +1134,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      // each producer warp, and in the E4M3 form the lanes of the one that copies the exponents
-      mbar_init(&ctl->full[i], kProducers + (S::kE4M3 ? 32 : 0));
+      // each producer warp, and the lanes of those that copy exponents (E4M3) or exponents and scales (INT4)
+      mbar_init(&ctl->full[i], kProducers + (S::kE4M3 ? 32 : S::kInt4 ? kProducers * 32 : 0));
       mbar_init(&ctl->empty[i], S::kGroupWarps);
     }
     for (int i = 0; i < S::kSlots; ++i) {
@@ -948,6 +1163,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int job_box = has_job ? job >> box_shift : 0, job_span = (job & (2 * copies - 1)) >> 1;
   const CUtensorMap* job_map = job & 1 ? &map_v : &map_k;
   const uint32_t job_at = smem_u32(smem) + (job & 1) * S::kTile + job_box * box * S::kRow + job_span * box * S::kSpan;
+  // INT4: the boxes that the lane's pieces of the scales belong to
+  constexpr int kScalePieces = S::kInt4 ? (S::kScales / 16 + 31) / 32 : 1;
+  const int pitch = scale_pitch(c.dim);
+  int scale_box[kScalePieces] = {};
+  if constexpr (S::kInt4) {
+    static_assert(kProducers == 2, "one for the keys' scales and one for the values'");
+#pragma unroll
+    for (int i = 0; i < kScalePieces; ++i) scale_box[i] = min((lane + i * 32) * 16 / (box * pitch), boxes - 1);
+  }
   pdl_begin();
 
   // The line's length and the place where this CTA's part begins.
@@ -1057,6 +1281,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               cp_async_arrive_noinc(bar);
             }
           }
+          if constexpr (S::kInt4) {
+            // the keys' by one warp, the values' by the other; a lane's pieces of 16 bytes lie in one box each
+            uint8_t* to = exps + stage * S::kExps;
+#pragma unroll
+            for (int i = 0; i < kScalePieces; ++i) {
+              const int y = __shfl_sync(0xffffffffu, row, scale_box[i]);
+              const int at = (lane + i * 32) * 16;
+              if (at < S::kTokens * pitch && (copied >> scale_box[i] & 1))
+                cp_async16(to + 2 * S::kTokens + me * S::kScales + at,
+                           (me ? c.v_scale : c.k_scale) + int64_t(y) * pitch + (at - scale_box[i] * box * pitch));
+            }
+            const int r = lane * 16 & (S::kTokens - 1), i = r >> row_shift;
+            const int y = __shfl_sync(0xffffffffu, row, i) + (r & (box - 1));
+            if (lane < S::kTokens / 16 && (copied >> i & 1))
+              cp_async16(to + me * S::kTokens + r, (me ? c.v_exp : c.k_exp) + y);
+            cp_async_arrive_noinc(bar);
+          }
         }
       }
       if (lane == 0) {
@@ -1104,7 +1345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wg = warp / S::kGroupWarps, row0 = (warp % S::kGroupWarps) * S::kPerWarp;
     bool timed_out = false;
     int joins = 0;  // the group's passes through the join buffer so far
-    Compute mine_w(row0, lane, box);
+    Compute mine_w(row0, lane, box, c.dim);
     for (; !walk.done(); it += walk.take, walk.next(a, segs), ++seg) {
       const int hb = walk.seg - walk.kv(head_blocks) * head_blocks, slot = seg % S::kSlots;
       const int n0 = unsigned(wg - it) % S::kGroups;  // the group's first tile of the segment
@@ -1121,6 +1362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tv.k = smem_u32(smem + size_t(stage) * S::kStage);
         tv.v = tv.k + S::kTile;
         tv.exps = exps + stage * S::kExps + row0;
+        tv.scales = exps + stage * S::kExps + 2 * S::kTokens + row0 * pitch;
         // the warp's tokens [from, to) of the tile lie in what is seen
         const int pos0 = (walk.span.tile0 + walk.tile + n) * S::kTokens + row0;
         const int from = max(0, walk.span.first - pos0), to = min(S::kPerWarp, walk.span.end - pos0);
@@ -1131,8 +1373,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (S::kPerWarp == 32 && !(copied & 2)) tv.seen &= 0xffffu;
         if (tv.seen != 0) {
           if (tv.seen != kAll) {
-            clear_rows<S>(tv.v, row0, box, tv.seen, lane);
-            fence_proxy_async_smem();  // before the next copy into these rows
+            if constexpr (S::kInt4) {
+              // (written by cp.async, like these stores: no other proxy)
+              clear_scales<S>(exps + stage * S::kExps + row0, pitch, row0, tv.seen, lane);
+            } else {
+              clear_rows<S>(tv.v, row0, box, tv.seen, lane);
+              fence_proxy_async_smem();  // before the next copy into these rows
+            }
             __syncwarp();
           }
           mine_w.tile(tv);
@@ -1273,15 +1520,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 bool cache_map(CUtensorMap* map, const void* base, const CacheDev& c, int box, int span, int spans) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t elem = c.e4m3 ? 1 : 2, row = c.dim * elem;
-  const cuuint64_t dims[3] = {spans > 1 ? span / elem : cuuint64_t(c.dim),
+  const cuuint64_t elem = c.rows == RowKind::kBf16 ? 2 : 1, row = row_bytes(c.rows, c.dim);
+  const cuuint64_t dims[3] = {spans > 1 ? span / elem : row / elem,
                               cuuint64_t(c.n_pages) * c.heads * c.page, spans > 1 ? row / span : 1};
   const cuuint64_t strides[2] = {row, cuuint64_t(span)};
   const cuuint32_t boxes[3] = {cuuint32_t(span / elem), cuuint32_t(box), cuuint32_t(spans)};
   const cuuint32_t ones[3] = {1, 1, 1};
-  return fn(map, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+  return fn(map, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
             dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            span == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+            : span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                         : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1325,14 +1575,19 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 //   4 108), 4 at widths above 128 (8 spill: 39.0 against 28.6).
 template <typename F>
 auto with_shape(const CacheDev& c, int group, F f) {
-  if (c.e4m3) {
-    if (c.dim <= 64) return group <= 4 ? f(Shape<true, 64, 4>{}) : f(Shape<true, 64, 8>{});
-    if (c.dim <= 128) return group <= 4 ? f(Shape<true, 128, 4>{}) : f(Shape<true, 128, 8>{});
-    return f(Shape<true, 256, 4>{});
+  if (c.rows == RowKind::kE4M3) {
+    if (c.dim <= 64) return group <= 4 ? f(Shape<RowKind::kE4M3, 64, 4>{}) : f(Shape<RowKind::kE4M3, 64, 8>{});
+    if (c.dim <= 128) return group <= 4 ? f(Shape<RowKind::kE4M3, 128, 4>{}) : f(Shape<RowKind::kE4M3, 128, 8>{});
+    return f(Shape<RowKind::kE4M3, 256, 4>{});
   }
-  if (c.dim <= 64) return group <= 8 ? f(Shape<false, 64, 8>{}) : f(Shape<false, 64, 16>{});
-  if (c.dim <= 128) return group <= 8 ? f(Shape<false, 128, 8>{}) : f(Shape<false, 128, 16>{});
-  return f(Shape<false, 256, 8>{});
+  if (c.rows == RowKind::kInt4) {
+    if (c.dim <= 64) return group <= 8 ? f(Shape<RowKind::kInt4, 64, 8>{}) : f(Shape<RowKind::kInt4, 64, 16>{});
+    if (c.dim <= 128) return group <= 8 ? f(Shape<RowKind::kInt4, 128, 8>{}) : f(Shape<RowKind::kInt4, 128, 16>{});
+    return f(Shape<RowKind::kInt4, 256, 8>{});
+  }
+  if (c.dim <= 64) return group <= 8 ? f(Shape<RowKind::kBf16, 64, 8>{}) : f(Shape<RowKind::kBf16, 64, 16>{});
+  if (c.dim <= 128) return group <= 8 ? f(Shape<RowKind::kBf16, 128, 8>{}) : f(Shape<RowKind::kBf16, 128, 16>{});
+  return f(Shape<RowKind::kBf16, 256, 8>{});
 }
 
 }  // namespace

@@ -1,16 +1,17 @@
 """The decode-step operators around the expert layer: a paged key-value cache (written as it is or
-quantised, and read back), the attention of one new token over it, and the norms, gate and residual
-between two blocks.  Argument marshalling only; include/libmoe.h states the operators.
+quantised, and read back) with its pages planned on the GPU, rotary positions on the way into it, the attention of
+one new token over it, and the norms, gate and residual between two blocks.  Argument marshalling only;
+include/libmoe.h states the operators.
 """
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
 from . import binding as _b
-from .binding import MOE_BF16, MOE_E4M3, MOE_F32
+from .binding import MOE_BF16, MOE_E4M3, MOE_F32, MOE_INT4
 
 # A decode step calls these operators a few times a layer with microseconds of GPU work each, so what
 # the host spends on a call counts: each tensor is looked at once, and only with the cheap accessors.
@@ -24,7 +25,8 @@ _devices = 0  # of the process; 0: not counted yet
 class MoeKvCacheC(ctypes.Structure):
     _fields_ = [("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
-                ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p)]
+                ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
 
 
 class KVCache:
@@ -32,28 +34,37 @@ class KVCache:
 
     k, v [n_pages, n_kv_heads, page_size, head_dim]: bf16, or E4M3 codes (uint8 or
     torch.float8_e4m3fn) with their rows' exponents k_exp, v_exp [n_pages, n_kv_heads, page_size]
-    uint8.  Pages are handed out by the caller: position p of sequence s is in row p % page_size of
-    page page_table[s, p // page_size]."""
+    uint8, or 4-bit codes (uint8, [.., head_dim / 2]) with exponents and the scales of 16 elements each, k_scale,
+    v_scale [n_pages, n_kv_heads, page_size, 4 ceil(head_dim / 64)] uint8.  Pages are handed out by the caller (or by
+    page_plan): position p of sequence s is in row p % page_size of page page_table[s, p // page_size]."""
 
-    def __init__(self, k, v, k_exp=None, v_exp=None):
-        e4m3 = k.dtype in (torch.uint8, torch.float8_e4m3fn)
-        if not e4m3 and k.dtype != torch.bfloat16:
-            raise ValueError(f"a cache holds bf16 values or E4M3 codes, not {k.dtype}")
+    def __init__(self, k, v, k_exp=None, v_exp=None, k_scale=None, v_scale=None):
+        int4 = k_scale is not None or v_scale is not None
+        e4m3 = not int4 and k.dtype in (torch.uint8, torch.float8_e4m3fn)
+        if not e4m3 and k.dtype != (torch.uint8 if int4 else torch.bfloat16):
+            raise ValueError(f"a cache holds bf16 values, E4M3 codes or (with scales) 4-bit codes, not {k.dtype}")
         if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype:
             raise ValueError("k and v are [n_pages, n_kv_heads, page_size, head_dim] of one type")
-        if e4m3:
+        if e4m3 or int4:
             for t in (k_exp, v_exp):
                 if t is None or t.dtype != torch.uint8 or t.shape != k.shape[:3]:
-                    raise ValueError("an E4M3 cache needs k_exp and v_exp, uint8 [n_pages, n_kv_heads, page_size]")
+                    raise ValueError("an E4M3 or 4-bit cache needs k_exp and v_exp, uint8 [n_pages, n_kv_heads, page_size]")
         elif k_exp is not None or v_exp is not None:
             raise ValueError("a bf16 cache has no exponents")
-        if any(t is not None and t.device != k.device for t in (v, k_exp, v_exp)):
+        if int4:
+            scales = (*k.shape[:3], _scale_pitch(2 * k.shape[3]))
+            for t in (k_scale, v_scale):
+                if t is None or t.dtype != torch.uint8 or t.shape != scales:
+                    raise ValueError(f"a 4-bit cache needs k_scale and v_scale, uint8 {list(scales)}")
+        if any(t is not None and t.device != k.device for t in (v, k_exp, v_exp, k_scale, v_scale)):
             raise ValueError("a cache's pools lie on one device")
-        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.k, self.v, self.k_exp, self.v_exp, self.k_scale, self.v_scale = k, v, k_exp, v_exp, k_scale, v_scale
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
-        self.dtype = MOE_E4M3 if e4m3 else MOE_BF16
+        if int4:
+            self.head_dim *= 2
+        self.dtype = MOE_INT4 if int4 else MOE_E4M3 if e4m3 else MOE_BF16
         self.c = MoeKvCacheC(self.n_pages, self.page_size, self.n_kv_heads, self.head_dim, self.dtype, _b._ptr(k),
-                             _b._ptr(v), _b._ptr(k_exp), _b._ptr(v_exp))
+                             _b._ptr(v), _b._ptr(k_exp), _b._ptr(v_exp), _b._ptr(k_scale), _b._ptr(v_scale))
         self.ref = ctypes.byref(self.c)
         self.device = k.get_device()
 
@@ -65,10 +76,22 @@ class KVCache:
         if dtype == MOE_BF16:
             k, v = (torch.empty(shape, dtype=torch.bfloat16, device=device) for _ in range(2))
             return cls(k, v)
-        if dtype != MOE_E4M3:
-            raise ValueError("a cache is MOE_BF16 or MOE_E4M3")
-        k, v = (torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2))
-        return cls(k, v, *(torch.empty(shape[:3], dtype=torch.uint8, device=device) for _ in range(2)))
+        if dtype not in (MOE_E4M3, MOE_INT4):
+            raise ValueError("a cache is MOE_BF16, MOE_E4M3 or MOE_INT4")
+        rows = shape[:3]
+
+        def pair(*last):
+            return [torch.empty((*rows, *last), dtype=torch.uint8, device=device) for _ in range(2)]
+
+        if dtype == MOE_E4M3:
+            return cls(*pair(head_dim), *pair())
+        if head_dim % 32 != 0:
+            raise ValueError("a 4-bit cache's head_dim is a multiple of 32")
+        return cls(*pair(head_dim // 2), *pair(), *pair(_scale_pitch(head_dim)))
+
+
+def _scale_pitch(head_dim: int) -> int:
+    return -(-head_dim // 64) * 4
 
 
 def _misfit(name: str, t: torch.Tensor, what: str):
@@ -206,6 +229,204 @@ def attn_decode(q: torch.Tensor, cache: KVCache, lens: torch.Tensor, page_table:
     if rc:
         raise _b.MoeError(rc, "moe_attn_decode")
     return out
+
+
+class PagePlan(NamedTuple):
+    """What page_plan returns: of each new token its sequence, position and slot (page * page_size + row), -1 behind the
+    last; where each sequence's tokens begin; the lengths and the count of free pages afterwards."""
+    seq: torch.Tensor
+    pos: torch.Tensor
+    slot: torch.Tensor
+    starts: torch.Tensor
+    lens: torch.Tensor
+    n_free: torch.Tensor
+
+
+def pages_workspace(B: int, device="cuda") -> torch.Tensor:
+    """Workspace of page_plan and page_release for up to B sequences (one call at a time)."""
+    n = int(_b.lib().moe_pages_workspace_bytes(B))
+    if n == 0:
+        raise _b.MoeError(-2, "moe_pages_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _ints(name: str, t: torch.Tensor, n: int, dev: int) -> int:
+    if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        raise _misfit(name, t, f"int32 [{n}], contiguous")
+    return t.data_ptr()
+
+
+def _pool(lens, page_table, free_pages, n_free, ws, lens_out, n_free_out):
+    """What page_plan and page_release share: sizes, addresses, and the outputs (in place where none are given)."""
+    dev = page_table.get_device()
+    if dev < 0:
+        raise _misfit("page_table", page_table, "int32 [sequences, pages], contiguous and on a GPU")
+    if _devices != 1:
+        _check_device(dev)
+    table, B, width, wp, wn = _table(page_table, ws, dev)
+    if free_pages.dim() != 1:
+        raise _misfit("free_pages", free_pages, "int32 [pages]")
+    n = free_pages.shape[0]
+    lens_out = lens if lens_out is None else lens_out
+    n_free_out = n_free if n_free_out is None else n_free_out
+    return (dev, B, width, table, _ints("lens", lens, B, dev), _ints("free_pages", free_pages, n, dev), n,
+            _ints("n_free", n_free, 1, dev), lens_out, _ints("lens_out", lens_out, B, dev), n_free_out,
+            _ints("n_free_out", n_free_out, 1, dev), wp, wn)
+
+
+def page_plan(lens: torch.Tensor, new_tokens: Optional[torch.Tensor], page_table: torch.Tensor, free_pages: torch.Tensor,
+              n_free: torch.Tensor, page_size: int, n_pages: int, max_tokens: int, ws: torch.Tensor,
+              lens_out: Optional[torch.Tensor] = None, n_free_out: Optional[torch.Tensor] = None,
+              starts: Optional[torch.Tensor] = None, seq: Optional[torch.Tensor] = None,
+              pos: Optional[torch.Tensor] = None, slot: Optional[torch.Tensor] = None) -> PagePlan:
+    """Room for new_tokens[b] (None: one) more tokens of each sequence, which has lens[b] in the cache: pages from the
+    stack free_pages [n_pages], whose first n_free[0] entries are free, into page_table [B, max_pages], and the list of
+    all new tokens' sequences, positions and slots, padded to max_tokens.  lens and n_free are updated in place unless
+    lens_out and n_free_out are given."""
+    (dev, B, width, table, lp, fp, n, np_, lens_out, lop, n_free_out, nop, wp, wn) = _pool(
+        lens, page_table, free_pages, n_free, ws, lens_out, n_free_out)
+    if n != n_pages:
+        raise _misfit("free_pages", free_pages, f"int32 [{n_pages}], contiguous")
+    new = None if new_tokens is None else _ints("new_tokens", new_tokens, B, dev)
+    if max_tokens < 0:
+        raise ValueError("max_tokens is 0 or more")
+
+    def out(name, t, count):
+        if t is None:
+            t = torch.empty(count, dtype=torch.int32, device=page_table.device)
+        return t, _ints(name, t, count, dev)
+
+    starts, sp = out("starts", starts, B + 1)
+    seq, qp = out("seq", seq, max_tokens)
+    pos, pp = out("pos", pos, max_tokens)
+    slot, tp = out("slot", slot, max_tokens)
+    rc = _b.lib().moe_page_plan(lp, new, B, table, width, fp, np_, n, page_size, max_tokens, lop, nop, sp, qp, pp, tp, wp,
+                                wn, _raw_stream(dev))
+    if rc:
+        raise _b.MoeError(rc, "moe_page_plan")
+    return PagePlan(seq, pos, slot, starts, lens_out, n_free_out)
+
+
+def page_release(lens: torch.Tensor, ended: torch.Tensor, page_table: torch.Tensor, free_pages: torch.Tensor,
+                 n_free: torch.Tensor, page_size: int, ws: torch.Tensor, lens_out: Optional[torch.Tensor] = None,
+                 n_free_out: Optional[torch.Tensor] = None):
+    """The pages of sequences with ended[b] (bool or uint8) back on the stack free_pages, their lengths 0.  Returns
+    (lens, n_free): updated in place unless lens_out and n_free_out are given."""
+    (dev, B, width, table, lp, fp, n, np_, lens_out, lop, n_free_out, nop, wp, wn) = _pool(
+        lens, page_table, free_pages, n_free, ws, lens_out, n_free_out)
+    if (ended.dtype not in (torch.bool, torch.uint8) or ended.shape != (B,) or ended.get_device() != dev
+            or not ended.is_contiguous()):
+        raise _misfit("ended", ended, f"bool or uint8 [{B}], contiguous")
+    rc = _b.lib().moe_page_release(lp, ended.data_ptr(), B, table, width, fp, np_, n, page_size, lop, nop, wp, wn,
+                                   _raw_stream(dev))
+    if rc:
+        raise _b.MoeError(rc, "moe_page_release")
+    return lens_out, n_free_out
+
+
+class MoeRopeC(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("magnitude", ctypes.c_float),
+                ("turns", ctypes.c_void_p)]
+
+
+class Rope:
+    """Rotary positions' frequencies on the device.  dim: the elements of each head that are turned (a multiple of 8);
+    interleaved: pairs are elements 2i and 2i + 1, else i and i + dim / 2.  scaling: "none", or how frequencies trained
+    for a context of `original` positions are changed for one `factor` times as long: "linear", "base", "by_index" (pairs
+    with more than `high` turns in the original context stay, those below `low` are slowed, between by their index; with
+    a magnitude) or "by_turns" (between by their turns).  frequencies: radians a position of each pair, in place
+    of all of that, with `magnitude` on cosine and sine."""
+    SCALINGS = ("none", "linear", "base", "by_index", "by_turns")
+
+    def __init__(self, dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, original: float = 4096.0, low: float = 1.0, high: float = 32.0,
+                 frequencies: Optional[Sequence[float]] = None, magnitude: Optional[float] = None, device="cuda"):
+        if dim <= 0 or dim % 8 != 0 or dim > 256:
+            raise ValueError("dim is a multiple of 8, from 8 to 256")
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling is one of {', '.join(self.SCALINGS)}")
+        turns, own = (ctypes.c_uint64 * (dim // 2))(), ctypes.c_float(1.0)
+        if frequencies is None:
+            rc = _b.lib().moe_rope_frequencies(dim, base, self.SCALINGS.index(scaling), factor, original, low, high, turns,
+                                               ctypes.byref(own))
+        else:
+            if scaling != "none":
+                raise ValueError("frequencies are given, or made by a scaling")
+            given = [float(f) for f in frequencies]
+            if len(given) != dim // 2:
+                raise ValueError(f"a frequency for each of {dim // 2} pairs")
+            rc = _b.lib().moe_rope_turns((ctypes.c_double * len(given))(*given), len(given), turns)
+        if rc:
+            raise _b.MoeError(rc, "moe_rope_frequencies" if frequencies is None else "moe_rope_turns")
+        self.dim, self.interleaved = dim, bool(interleaved)
+        self.magnitude = own.value if magnitude is None else float(magnitude)
+        # torch has no arithmetic for uint64 everywhere: the same bits
+        self.turns = torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        self.device = self.turns.get_device()
+        self.c = MoeRopeC(dim, int(self.interleaved), self.magnitude, _b._ptr(self.turns))
+        self.ref = ctypes.byref(self.c)
+
+
+def _heads(name: str, t: torch.Tensor, dev: int, code_of=_CODES):
+    """Type code, shape and row stride of t [tokens, heads, dim]."""
+    code = code_of.get(t.dtype)
+    if code is None or t.dim() != 3 or t.get_device() != dev:
+        raise _misfit(name, t, "bf16 or fp32 [tokens, heads, head_dim]")
+    T, heads, dim = t.shape
+    return code, T, heads, dim, _row_stride(t, name, heads, dim)
+
+
+def rope(x: torch.Tensor, table: Rope, pos: torch.Tensor, out: Optional[torch.Tensor] = None,
+         inverse: bool = False) -> torch.Tensor:
+    """x [tokens, heads, head_dim] bf16 or fp32 (rows may be slices of a fused projection's output) with the first
+    table.dim elements of each head turned by its token's position pos[t]; inverse: turned back.  out may be x."""
+    dev = table.device
+    if _devices != 1:
+        _check_device(dev)
+    code, T, heads, dim, stride = _heads("x", x, dev)
+    pp = _ints("pos", pos, T, dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.dtype is not x.dtype or out.shape != x.shape:
+        raise _misfit("out", out, f"{x.dtype} {list(x.shape)}, as x")
+    out_stride = _heads("out", out, dev)[4]
+    rc = _b.lib().moe_rope_apply(table.ref, x.data_ptr(), stride, out.data_ptr(), out_stride, code, T, heads, dim, pp,
+                                 int(inverse), _raw_stream(dev))
+    if rc:
+        raise _b.MoeError(rc, "moe_rope_apply")
+    return out
+
+
+def rope_kv_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVCache, table: Rope, pos: torch.Tensor,
+                  slot: torch.Tensor, ws: torch.Tensor, q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """q [T, n_heads, head_dim] and k [T, n_kv_heads, head_dim] turned by their tokens' positions pos[t]; the keys and v
+    into the cache at slot[t] (page * page_size + row, as page_plan gives them; negative: not written).  q, k and v bf16
+    or fp32, slices of a fused projection's output as it lies.  Returns q_out, bf16, which may be q."""
+    dev, dim = cache.device, cache.head_dim
+    if _devices != 1:
+        _check_device(dev)
+    code, T, heads, q_dim, q_stride = _heads("q", q, dev)
+    if q_dim != dim or table.device != dev:
+        raise _misfit("q", q, f"bf16 or fp32 [tokens, heads, {dim}]")
+    shape = (T, cache.n_kv_heads, dim)
+    if k.dtype is not q.dtype or k.shape != shape or k.get_device() != dev:
+        raise _misfit("k", k, f"{q.dtype} {list(shape)}")
+    if v.dtype is not q.dtype or v.shape != shape or v.get_device() != dev:
+        raise _misfit("v", v, f"{q.dtype} {list(shape)}")
+    pp, sp = _ints("pos", pos, T, dev), _ints("slot", slot, T, dev)
+    if ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise _misfit("ws", ws, "uint8, contiguous")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    elif q_out.dtype is not torch.bfloat16 or q_out.shape != q.shape or q_out.get_device() != dev:
+        raise _misfit("q_out", q_out, f"bf16 {list(q.shape)}")
+    rc = _b.lib().moe_rope_kv_write(table.ref, cache.ref, q.data_ptr(), q_stride, heads, q_out.data_ptr(),
+                                    _row_stride(q_out, "q_out", heads, dim), k.data_ptr(), v.data_ptr(), code,
+                                    _row_stride(k, "k", shape[1], dim), _row_stride(v, "v", shape[1], dim), T, pp, sp,
+                                    ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if rc:
+        raise _b.MoeError(rc, "moe_rope_kv_write")
+    return q_out
 
 
 def block_norm(residual: torch.Tensor, w_pre: Optional[torch.Tensor], y: Optional[torch.Tensor] = None,
