@@ -57,23 +57,15 @@
 // through TMEM.  Keys and values reach the registers by ldmatrix from the swizzled tiles, the
 // values transposed.
 #include "batches.cuh"
-#include "decoder.cuh"
+#include "kv_rows.cuh"
 #include "tcgen05.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;      // compute
-constexpr int kProducers = 2;  // start copies
-constexpr int kQueryWarp = kWarps + kProducers;
-constexpr int kQueryWarps = 2;  // the second also zeroes the rows of empty sequences
-constexpr int kEndWarp = kWarps + 4;  // the first of those that end segments
-constexpr int kEndThreads = 128;
-constexpr int kThreads = kEndWarp * 32 + kEndThreads;
-// Registers a thread of the four warpgroups (compute twice, producers, segment ends); the launch gives
-// each 128, and the shares add up to that.
-constexpr int kComputeRegs = 160, kProducerRegs = 80, kEndRegs = 112;
-static_assert(2 * kComputeRegs + kProducerRegs + kEndRegs <= 4 * (65536 / kThreads), "registers");
+constexpr int kProducers = 2;    // start copies
+constexpr int kQueryWarps = 2;   // the second also zeroes the rows of empty sequences
+constexpr int kEndThreads = 128;  // end segments
 constexpr size_t kSmemLimit = 227 * 1024;
 constexpr int kMaxCtas = 256;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -85,6 +77,19 @@ template <RowKind kRows_, int kDim_, int kHeads_>
 struct Shape {
   static constexpr RowKind kRows = kRows_;
   static constexpr bool kE4M3 = kRows == RowKind::kE4M3, kInt4 = kRows == RowKind::kInt4;
+  // The warps: those that compute, then producers and queries, then those that end segments.  INT4 takes its codes apart
+  // in the computing warps and is bound by what they issue, so it has twelve where their registers allow.
+  static constexpr int kWarps = kInt4 && kDim_ * kHeads_ < 0 ? 12 : 8;
+  static constexpr int kQueryWarp = kWarps + kProducers;
+  static constexpr int kEndWarp = kQueryWarp + kQueryWarps;  // the first of those that end segments
+  static constexpr int kThreads = kEndWarp * 32 + kEndThreads;
+  // Registers a thread of the warpgroups (compute, producers and queries, segment ends); the launch gives each
+  // kLaunchRegs, and the shares add up to that.
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+  static constexpr int kComputeRegs = kWarps == 8 ? 160 : 104;
+  static constexpr int kProducerRegs = kWarps == 8 ? 80 : 80, kEndRegs = kWarps == 8 ? 112 : 88;
+  static constexpr bool kQueriesStay = kInt4;
+  static_assert(kWarps / 4 * kComputeRegs + kProducerRegs + kEndRegs <= kThreads / 128 * kLaunchRegs, "registers");
   static constexpr int kDim = kDim_;      // head_dim rounded up to 64, 128 or 256 (copies fill with zeros)
   static constexpr int kHeads = kHeads_;  // query heads of a segment
   static constexpr int kRow = kE4M3 ? kDim : kInt4 ? kDim / 2 : kDim * 2;  // bytes
@@ -329,7 +334,8 @@ struct Parts {
 struct TileView {
   uint32_t k, v;          // shared-memory addresses of the key and value tiles
   const uint8_t* exps;    // of the keys; the values' follow kTokens further
-  const uint8_t* scales;  // of the keys; the values' follow kScales further
+  uint32_t exps_at, scales_at;  // INT4: shared-memory addresses of them, and of the keys' scales; the values'
+                                // scales follow kScales further
   uint32_t seen;          // a bit for each of the warp's tokens
 };
 
@@ -378,7 +384,7 @@ template <typename S>
 __device__ __forceinline__ void clear_scales(uint8_t* exps, int pitch, int row0, uint32_t seen, int lane) {
   static_assert(!S::kInt4 || S::kPerWarp == 32, "a lane a row");
   if (seen >> lane & 1) return;
-  exps[S::kTokens + lane] = 15;
+  exps[S::kTokens + lane] = kInt4Zero;
   uint32_t* s = reinterpret_cast<uint32_t*>(exps - row0 + 2 * S::kTokens + S::kScales + (row0 + lane) * pitch);
   for (int w = 0; w < pitch / 4; ++w) s[w] = 0u;
 }
@@ -447,18 +453,18 @@ struct Bf16Operands {
 //
 // Rows that a warp does not see have their values' scales and exponents set to what makes u = 0, whatever the codes are.
 // An exponent byte of 255 makes u an infinity or a NaN, and the values inf - inf.
-constexpr uint32_t kInt4Zero = 15;  // the exponent byte that makes u = 0 of scale byte 0
-
 template <typename S>
 struct Int4Operands {
   static constexpr int kKS = S::kDim / 16, kNB = S::kHeads / 8;
   static constexpr int kWords = S::kDim / 32;       // of a lane's quarter of a row, eight codes each
   static constexpr int kPitchWords = S::kDim / 64;  // of a row's scales
   uint32_t k_at, k_flip, v_at, v_flip;  // rows and swizzle of the lane's key words and ldmatrix rows
-  int pitch, k_col, g, t;
+  uint32_t k_scale_at, v_scale_at;      // of the lane's first rows
+  int pitch, g, t;
   uint32_t pick[2];                     // byte selectors for the scales of two tokens
   uint32_t word[2][kWords], unit[2][kWords / 2], minus[2][kWords / 2];  // key rows g and g + 8
   uint32_t chunk[4], v_scale[4][kPitchWords], v_exp[2];
+  uint32_t mask, one;                   // constants that the compiler is to keep in registers
 
   // 16-byte chunk i of row r lies at chunk i ^ flip(r)
   static __device__ __forceinline__ uint32_t swizzle(int r) {
@@ -471,9 +477,12 @@ struct Int4Operands {
     v_at = uint32_t(v_row * S::kRow);
     v_flip = swizzle(v_row) ^ (lane >> 4);
     pitch = scale_pitch(dim);
+    mask = kept(0x00780078u);
+    one = kept(0x43004300u);
     // a quarter past the row's end holds no codes that count (the queries there are 0): any scale will do
     const int col = t * (S::kDim / 64);
-    k_col = col * 16 < dim ? col : 0;
+    k_scale_at = uint32_t(g * pitch + (col * 16 < dim ? col : 0));
+    v_scale_at = uint32_t(S::kScales + 2 * t * pitch);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t k = 2 * i + (g >> 2);
@@ -506,28 +515,31 @@ struct Int4Operands {
       }
   }
 
+  static __device__ __forceinline__ uint32_t kept(uint32_t x) {
+    asm volatile("" : "+r"(x));
+    return x;
+  }
+  static __device__ __forceinline__ uint32_t lds8(uint32_t at) {
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t lds16(uint32_t at) {
+    uint16_t r;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at) : "memory");
+    return r;
+  }
+  static __device__ __forceinline__ uint32_t lds32(uint32_t at) {
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    return r;
+  }
   // __byte_perm, whose selectors know no signs
   static __device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t sel) {
     uint32_t r;
     asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
     return r;
   }
-  static __device__ __forceinline__ uint32_t scaled(uint32_t x, uint32_t u, uint32_t m) {
-    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&u),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&m));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-  static __device__ __forceinline__ uint32_t times_minus_192(uint32_t u) {
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), __float2bfloat162_rn(-192.0f));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-  // Codes 2j and 2j + 1 of both halves, as 192 + 8n.
-  static __device__ __forceinline__ void codes(uint32_t w, int j, uint32_t& a, uint32_t& b) {
-    if (j == 1) w = __byte_perm(w, 0u, 0x2301);  // each half's bytes exchanged: turned by 8
-    a = (w & 0x00780078u) | 0x43004300u;
-    b = (w >> 4 & 0x00780078u) | 0x43004300u;
-  }
-
   __device__ __forceinline__ void key(const TileView& tv, int mt, int ks, uint32_t (&r)[4]) {
     if (ks == 0) {
 #pragma unroll
@@ -547,16 +559,13 @@ struct Int4Operands {
                          : "r"(at + (((t * (kWords / 4) + i) ^ k_flip) << 4))
                          : "memory");
         }
-        const uint8_t* s = tv.scales + (row + g) * pitch + k_col;
-        uint32_t bytes;
-        if constexpr (S::kDim == 64) bytes = *s;
-        else if constexpr (S::kDim == 128) bytes = *reinterpret_cast<const uint16_t*>(s);
-        else bytes = *reinterpret_cast<const uint32_t*>(s);
-        const uint32_t e = (uint32_t(tv.exps[row + g]) - kInt4Zero) * 0x00800080u;
+        const uint32_t s = tv.scales_at + k_scale_at + uint32_t(row * pitch);
+        const uint32_t bytes = S::kDim == 64 ? lds8(s) : S::kDim == 128 ? lds16(s) : lds32(s);
+        const uint32_t e = (lds8(tv.exps_at + row + g) - kInt4Zero) * 0x00800080u;
 #pragma unroll
         for (int i = 0; i < kWords / 2; ++i) {
           unit[h][i] = __byte_perm(bytes, 0u, 0x4040 + i * 0x0101) * 16u + e;
-          minus[h][i] = times_minus_192(unit[h][i]);
+          minus[h][i] = int4_minus_192(unit[h][i]);
         }
       }
     }
@@ -564,9 +573,9 @@ struct Int4Operands {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t a, b;
-      codes(word[h][w], ks & 1, a, b);
-      r[h] = scaled(a, unit[h][w / 2], minus[h][w / 2]);
-      r[2 + h] = scaled(b, unit[h][w / 2], minus[h][w / 2]);
+      int4_pair(word[h][w], ks & 1, mask, one, a, b);
+      r[h] = int4_fma(a, unit[h][w / 2], minus[h][w / 2]);
+      r[2 + h] = int4_fma(b, unit[h][w / 2], minus[h][w / 2]);
     }
   }
 
@@ -575,13 +584,17 @@ struct Int4Operands {
     if (md == 0) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-        const uint8_t* s = tv.scales + S::kScales + (mt * 16 + 2 * t + (i & 1) + (i >> 1) * 8) * pitch;
+        const uint32_t s = tv.scales_at + v_scale_at + uint32_t((mt * 16 + (i & 1) + (i >> 1) * 8) * pitch);
+        if constexpr (S::kDim == 128) {
+          asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v_scale[i][0]), "=r"(v_scale[i][1]) : "r"(s) : "memory");
+        } else {
 #pragma unroll
-        for (int w = 0; w < kPitchWords; ++w) v_scale[i][w] = reinterpret_cast<const uint32_t*>(s)[w];
+          for (int w = 0; w < kPitchWords; ++w) v_scale[i][w] = lds32(s + 4 * w);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t e = *reinterpret_cast<const uint16_t*>(tv.exps + S::kTokens + mt * 16 + 2 * t + i * 8);
+        const uint32_t e = lds16(tv.exps_at + S::kTokens + mt * 16 + 2 * t + i * 8);
         v_exp[i] = __byte_perm(e, 0u, 0x4140) * 128u - kInt4Zero * 0x00800080u;
       }
     }
@@ -590,11 +603,11 @@ struct Int4Operands {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // tokens 2t and 2t + 1, and 8 further
       const uint32_t u = permute(v_scale[2 * i][c / 2], v_scale[2 * i + 1][c / 2], pick[cc]) * 16u + v_exp[i];
-      const uint32_t m = times_minus_192(u);
+      const uint32_t m = int4_minus_192(u);
       uint32_t a, b;
-      codes(chunk[2 * cc + i], md & 1, a, b);
-      r[2 * i] = scaled(a, u, m);
-      r[2 * i + 1] = scaled(b, u, m);
+      int4_pair(chunk[2 * cc + i], md & 1, mask, one, a, b);
+      r[2 * i] = int4_fma(a, u, m);
+      r[2 * i + 1] = int4_fma(b, u, m);
     }
   }
   template <typename Acc>
@@ -615,7 +628,8 @@ template <typename S>
 struct WarpBf16 {
   using Operands = std::conditional_t<S::kInt4, Int4Operands<S>, Bf16Operands<S>>;
   static constexpr int kMT = S::kPerWarp / 16, kKS = S::kDim / 16, kNB = S::kHeads / 8;
-  uint32_t q[kKS][kNB][2];
+  uint32_t q[kKS][kNB][2];  // kQueriesStay: read where they are needed
+  uint32_t queries_at;
   float m[kNB][2], sum[kNB][2], acc[kKS][kNB][4];
   float factor;  // scores to base-2 exponents
   Operands operands;
@@ -632,6 +646,7 @@ struct WarpBf16 {
 
   __device__ __forceinline__ void begin(const uint8_t* queries, int lane) {
     factor = *reinterpret_cast<const float*>(queries + S::kQueryRegs * 128);
+    queries_at = smem_u32(queries) + lane * 16;
 #pragma unroll
     for (int nb = 0; nb < kNB; ++nb) {
       m[nb][0] = m[nb][1] = -INFINITY;
@@ -641,7 +656,7 @@ struct WarpBf16 {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[ks][nb][i] = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < kKS; ks += 2) {
+      for (int ks = 0; ks < kKS && !S::kQueriesStay; ks += 2) {
         const uint4 u = *reinterpret_cast<const uint4*>(queries + ((nb * kKS + ks) / 2 * 32 + lane) * 16);
         q[ks][nb][0] = u.x, q[ks][nb][1] = u.y, q[ks + 1][nb][0] = u.z, q[ks + 1][nb][1] = u.w;
       }
@@ -661,6 +676,15 @@ struct WarpBf16 {
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         uint32_t r[4];
+        if constexpr (S::kQueriesStay) {
+          if (ks % 2 == 0)
+#pragma unroll
+            for (int nb = 0; nb < kNB; ++nb)
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(q[ks][nb][0]), "=r"(q[ks][nb][1]), "=r"(q[ks + 1][nb][0]), "=r"(q[ks + 1][nb][1])
+                           : "r"(queries_at + (nb * kKS + ks) / 2 * 512)
+                           : "memory");
+        }
         operands.key(tv, mt, ks, r);
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) mma_bf16_16x8x16(ks & 1 ? s2[nb] : s[mt][nb], r, q[ks][nb][0], q[ks][nb][1]);
@@ -670,8 +694,20 @@ struct WarpBf16 {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float x = (s[mt][nb][i] + s2[nb][i]) * factor;
-          s[mt][nb][i] = seen >> (mt * 16 + (i >> 1) * 8) & 1 ? x : -INFINITY;
+          if constexpr (S::kInt4) s[mt][nb][i] = x;
+          else s[mt][nb][i] = seen >> (mt * 16 + (i >> 1) * 8) & 1 ? x : -INFINITY;
         }
+    }
+    if constexpr (S::kInt4) {  // the masks are a part of the time here, and few tiles need them
+      if (tv.seen != 0xffffffffu >> (32 - S::kPerWarp)) {
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+          for (int nb = 0; nb < kNB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!(seen >> (mt * 16 + (i >> 1) * 8) & 1)) s[mt][nb][i] = -INFINITY;
+      }
     }
     float base[kNB][2], fix[kNB][2];
     bool moved = false;
@@ -1117,7 +1153,7 @@ __device__ __forceinline__ void for_constants(std::integer_sequence<int, I...>, 
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(S::kThreads, 1)
     k_attn_decode(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   int box, int copies, int page_boxes, uint32_t page_magic, int group, int head_blocks) {
   using Control = typename S::Control;
@@ -1140,7 +1176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&ctl->q_full[i], 1);
-      mbar_init(&ctl->q_empty[i], kWarps);
+      mbar_init(&ctl->q_empty[i], S::kWarps);
     }
     for (int i = 0; i < S::kGroups; ++i) {
       mbar_init(&ctl->join_full[i], S::kGroupWarps);
@@ -1154,7 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // What a producer warp needs that no earlier kernel writes: lane's copy of every tile (one of keys or
   // values, one span or all, one box).
-  const int me = warp - kWarps;
+  const int me = warp - S::kWarps;
   const int boxes = S::kTokens / box;    // of a tile: 1, 2, 4 or 8
   const int box_shift = __ffs(2 * copies) - 1, row_shift = __ffs(box) - 1;
   const uint32_t job_bytes = uint32_t(box * S::kRow) >> (box_shift - 1);
@@ -1175,7 +1211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_begin();
 
   // The line's length and the place where this CTA's part begins.
-  const int per = (a.B + kThreads - 1) / kThreads;
+  const int per = (a.B + S::kThreads - 1) / S::kThreads;
   const int b_lo = min(a.B, int(threadIdx.x) * per), b_hi = min(a.B, b_lo + per);
   int mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
@@ -1192,7 +1228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   int total = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < S::kThreads / 32; ++w) {
     if (w == warp) upto += total;
     total += ctl->scan[w];
   }
@@ -1220,9 +1256,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   walk.start(a, ctl->b0, ctl->off0, lo, hi);
   int it = 0, seg = 0;
 
-  if (warp >= kWarps && warp < kEndWarp) {
-    fewer_registers<kProducerRegs>();
-    if (warp < kQueryWarp) {
+  if (warp >= S::kWarps && warp < S::kEndWarp) {
+    fewer_registers<S::kProducerRegs>();
+    if (warp < S::kQueryWarp) {
       // --------------------------------------------------------------- producers ------------
       bool ok = true;
       for (; ok && !walk.done(); walk.next(a, segs)) {
@@ -1310,7 +1346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       }
     } else {
-      if (warp == kQueryWarp + 1) {
+      if (warp == S::kQueryWarp + 1) {
         // ----------------------------------------- sequences without a token: zeros ---------
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
           if (span_of<S>(a, b).tiles != 0) continue;
@@ -1323,7 +1359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ------------------------------- queries, the segments in turn by the two warps -------
       for (; !walk.done(); walk.next(a, segs), ++seg) {
-        if (seg % kQueryWarps != warp - kQueryWarp) continue;
+        if (seg % kQueryWarps != warp - S::kQueryWarp) continue;
         const int kv = walk.kv(head_blocks), hb = walk.seg - kv * head_blocks, slot = seg % S::kSlots;
         if (!__all_sync(0xffffffffu, wait_part(&ctl->q_empty[slot], ((seg / S::kSlots) & 1) ^ 1, &ctl->abort))) {
           if (lane == 0) report_timeout_flag(a.table.status_flags, 41);
@@ -1339,21 +1375,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
-  if (warp < kWarps) {
+  if (warp < S::kWarps) {
     // ------------------------------------------------------------------ compute -------------
-    more_registers<kComputeRegs>();
+    more_registers<S::kComputeRegs>();
     const int wg = warp / S::kGroupWarps, row0 = (warp % S::kGroupWarps) * S::kPerWarp;
     bool timed_out = false;
     int joins = 0;  // the group's passes through the join buffer so far
     Compute mine_w(row0, lane, box, c.dim);
     for (; !walk.done(); it += walk.take, walk.next(a, segs), ++seg) {
       const int hb = walk.seg - walk.kv(head_blocks) * head_blocks, slot = seg % S::kSlots;
-      const int n0 = unsigned(wg - it) % S::kGroups;  // the group's first tile of the segment
+      const int n0 = unsigned(wg + S::kGroups - it % S::kGroups) % S::kGroups;  // the group's first tile of the segment
       if (!wait(&ctl->q_full[slot], (seg / S::kSlots) & 1, &ctl->abort)) timed_out = true;
       // (under a condition, n0 < walk.take, more registers spill: 16 heads, 64 x 8k bf16 68.1 us against 66.5)
       mine_w.begin(queries + slot * S::kQueries, lane);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->q_empty[slot]);
+      if (!S::kQueriesStay || n0 >= walk.take) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->q_empty[slot]);
+      }
       if (n0 >= walk.take) continue;
       TileView tv;
       for (int n = n0; n < walk.take; n += S::kGroups) {
@@ -1362,7 +1400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tv.k = smem_u32(smem + size_t(stage) * S::kStage);
         tv.v = tv.k + S::kTile;
         tv.exps = exps + stage * S::kExps + row0;
-        tv.scales = exps + stage * S::kExps + 2 * S::kTokens + row0 * pitch;
+        tv.exps_at = smem_u32(tv.exps);
+        tv.scales_at = tv.exps_at - row0 + 2 * S::kTokens + row0 * pitch;
         // the warp's tokens [from, to) of the tile lie in what is seen
         const int pos0 = (walk.span.tile0 + walk.tile + n) * S::kTokens + row0;
         const int from = max(0, walk.span.first - pos0), to = min(S::kPerWarp, walk.span.end - pos0);
@@ -1387,6 +1426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->empty[stage]);
       }
+      if (S::kQueriesStay && lane == 0) mbar_arrive(&ctl->q_empty[slot]);
       const int heads = min(S::kHeads, group - hb * S::kHeads);
       for_constants(std::make_integer_sequence<int, S::kPasses>{}, [&](auto pass) {
         constexpr int kPass = decltype(pass)::value;
@@ -1404,8 +1444,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------------------------------------------------------------- segment ends ------
-  fewer_registers<kEndRegs>();
-  const int tid = threadIdx.x - kEndWarp * 32;
+  fewer_registers<S::kEndRegs>();
+  const int tid = threadIdx.x - S::kEndWarp * 32;
   bool timed_out = false;
   int n_joints = 0;
   uint32_t phases = 0;  // a bit for each group: the parity of its next pass through the join buffer
@@ -1444,10 +1484,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (groups == (1u << S::kGroups) - 1) {
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) top_of(w);
+          for (int w = 0; w < S::kWarps; ++w) top_of(w);
           const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) add(w, base);
+          for (int w = 0; w < S::kWarps; ++w) add(w, base);
         } else {
           for (uint32_t left = groups; left; left &= left - 1)
 #pragma unroll
@@ -1544,7 +1584,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     cudaFuncAttributes f;
     attr = cudaFuncGetAttributes(&f, k_attn_decode<S>);
     // the warpgroups divide up what the launch gets: with less than they ask for they would wait for ever
-    if (attr == cudaSuccess && 4 * f.numRegs < 2 * kComputeRegs + kProducerRegs + kEndRegs)
+    if (attr == cudaSuccess && S::kThreads / 128 * f.numRegs < S::kWarps / 4 * S::kComputeRegs + S::kProducerRegs + S::kEndRegs)
       attr = cudaErrorInvalidConfiguration;
     if (attr == cudaSuccess)
       attr = cudaFuncSetAttribute(k_attn_decode<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
@@ -1563,7 +1603,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   // i / page_boxes = the high half of i * page_magic, for i below 2^32 / page_boxes: positions below 2^28
   // make at most 2^24 boxes of 16, and a page at most 256
   const uint32_t page_magic = uint32_t(((uint64_t(1) << 32) + page_boxes - 1) / page_boxes);
-  return launch_pdl(k_attn_decode<S>, dim3(ctas), dim3(kThreads), S::kSmem, s, a, mk, mv, box,
+  return launch_pdl(k_attn_decode<S>, dim3(ctas), dim3(S::kThreads), S::kSmem, s, a, mk, mv, box,
                     S::kSpans / spans, page_boxes, page_magic, group, (group + S::kHeads - 1) / S::kHeads);
 }
 

@@ -79,11 +79,8 @@ __global__ void __launch_bounds__(256) k_kv_read(CacheDev c, PageTable pt, int T
   for (int j = 0; j < kHeadsEach; ++j) {
     if (j >= heads) continue;
     const int64_t at = (int64_t(t) * c.heads + h0 + j) * c.dim + lane * 8;
-    float x[8];
-    k[j].values(row0 >= 0, x);
-    store_vec8(k_out + at, x);
-    v[j].values(row0 >= 0, x);
-    store_vec8(v_out + at, x);
+    k[j].store(k_out + at);
+    v[j].store(v_out + at);
   }
 }
 

@@ -6,10 +6,8 @@
 // significant bits): reading back adds none.
 //
 // INT4: e likewise with 105 (7 times the largest scale), then the smallest scale s of each 16 elements with
-// 7 s >= max|x 2^-e|, then n = x 2^-e / s to the nearest whole number, ties to even.  The quotient is found by a
-// reciprocal and put right by its remainder y - n s, which is exact in fp32 (n s is of 7 bits, and within a factor
-// of two of y or 0): so n does not depend on how the reciprocal is rounded.  n s 2^e has 7 significant bits, and is
-// exact in bf16 as well.
+// 7 s >= max|x 2^-e|, then n = x 2^-e / s to the nearest whole number, ties to even.  n s 2^e has 7 significant
+// bits, and is exact in bf16 as well.
 #pragma once
 
 #include "decoder.cuh"
@@ -46,19 +44,62 @@ __device__ __forceinline__ void values8(uint2 codes, float unit, float (&v)[8]) 
   }
 }
 
-// y / s to the nearest whole number of -7 .. 7, ties to even, plus 8.
-__device__ __forceinline__ uint32_t int4_code(float y, float s, float reciprocal) {
-  float n = rintf(y * reciprocal);
-  const float rest = fmaf(-n, s, y), over = fabsf(rest) - 0.5f * s;
-  const float odd = fabsf(n - 2.0f * rintf(0.5f * n));  // 0 or 1
-  if (over > 0.0f || (over == 0.0f && odd != 0.0f)) n += copysignf(1.0f, rest);
-  n = fminf(fmaxf(n, -kInt4Most), kInt4Most);
-  return __float_as_uint(n + (8388608.0f + 8.0f)) & 15u;  // 2^23: the whole number is in the low bits
+// The largest of magnitudes, NaN where one of them is (fmaxf would leave it out).
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-// Four codes a half, as two 16-bit words turned left by 3.
-__device__ __forceinline__ uint32_t int4_turned(uint32_t w) { return (w << 3 & 0xfff8fff8u) | (w >> 13 & 0x00070007u); }
-__device__ __forceinline__ uint32_t int4_turned_back(uint32_t w) { return (w >> 3 & 0x1fff1fffu) | (w << 13 & 0xe000e000u); }
+// The codes of eight elements, x_i / s to the nearest whole number of -7 .. 7, ties to even, plus 8, in the order of the
+// cache (s the scale times the row's power of two, which changes no rounding here).  With the reciprocal rounded to
+// nearest, the quotient put right by its remainder (exact, by a fused multiply-add) is the correctly rounded one
+// [Markstein 1990]; and that lies on the same side of a border k + 1/2 as the exact one, or on it with it: a border
+// times s has 7 bits, and the next fp32 number is further from it than the quotient's rounding reaches.  Added to
+// 1.5 * 2^23 + 8 it is rounded to a whole number, whose code stands in the low bits; multiply-adds put the eight side by
+// side, and what is above the low bits adds up to a constant.
+__device__ __forceinline__ uint32_t int4_codes(const float (&x)[8], float s, bool cut) {
+  constexpr float kWhole = 12582912.0f + 8.0f;
+  constexpr uint32_t kAbove = 0x4b400000u;  // 1.5 * 2^23's bits
+  const float reciprocal = __frcp_rn(s);
+  uint32_t w = 0u - kAbove * 0x11111111u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = x[i] * reciprocal;
+    float n = fmaf(fmaf(-q, s, x[i]), reciprocal, q);
+    if (cut) n = fminf(fmaxf(n, -kInt4Most), kInt4Most);
+    w += __float_as_uint(n + kWhole) << (4 * i);
+  }
+  return (w << 3 & 0xfff8fff8u) | (w >> 13 & 0x00070007u);
+}
+
+// A word of codes taken apart: element i and i + 4 of its eight in the halves of r[i], as bf16 numbers times u, where
+// u holds an eighth of the elements' unit (scale times the row's power of two) in both halves, and minus -192 u.  A code
+// c = n + 8 at mantissa bits 3 to 6 of a bf16 number 128 makes it 192 + 8n, and one fused multiply-add gives 8n u without
+// rounding (n u has 7 significant bits).  The cache's order of bits makes shifts unnecessary for four of the eight.
+__device__ __forceinline__ uint32_t int4_fma(uint32_t x, uint32_t u, uint32_t minus) {
+  const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&u),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&minus));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t int4_minus_192(uint32_t u) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u), __float2bfloat162_rn(-192.0f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Codes 2j and 2j + 1 of both halves, as 192 + 8n; mask 0x00780078 and one 0x43004300.
+__device__ __forceinline__ void int4_pair(uint32_t w, int j, uint32_t mask, uint32_t one, uint32_t& a, uint32_t& b) {
+  if (j == 1) w = __byte_perm(w, 0u, 0x2301);  // each half's bytes exchanged: turned by 8
+  const uint32_t x = w >> 4;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(a) : "r"(w), "r"(mask), "r"(one));  // (w & mask) | one
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(b) : "r"(x), "r"(mask), "r"(one));
+}
+// u of a scale byte and an exponent byte: the scale's three mantissa bits and four exponent bits moved to their places,
+// and the exponents added, all biased.  kInt4Zero with scale byte 0 gives u = 0, whatever the codes are; exponent 255 with
+// scale 127 a NaN, and then so are the values.
+constexpr uint32_t kInt4Zero = 15;
+__device__ __forceinline__ uint32_t int4_unit(uint32_t scale, uint32_t exp) {
+  return (scale * 16u + (exp - kInt4Zero) * 128u) * 0x00010001u;
+}
 
 // Writes one row, if `write` holds (the same for the lanes of a group; all lanes of the warp come here).  x: the
 // lane's eight elements, zeros past the row's end.
@@ -74,24 +115,20 @@ __device__ __forceinline__ void store_row(const CacheDev& c, uint8_t* pool, uint
     if (mine) *reinterpret_cast<uint2*>(pool + row * c.dim + lane * 8) = codes8(x, inverse_exp_value(e));
     if (lane == 0) exps[row] = uint8_t(e);
   } else {
-    uint32_t top = 0;  // largest magnitude's bits: an infinity's or a NaN's are above all numbers'
+    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    uint32_t row_top = top;
+    for (int i = 0; i < 8; ++i) top = max_or_nan(top, fabsf(x[i]));
+    top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    float row_top = top;
 #pragma unroll
-    for (int o = kLanes / 2; o > 1; o >>= 1) row_top = max(row_top, __shfl_xor_sync(0xffffffffu, row_top, o));
+    for (int o = kLanes / 2; o > 1; o >>= 1) row_top = max_or_nan(row_top, __shfl_xor_sync(0xffffffffu, row_top, o));
     if (!write) return;
-    const bool lost = row_top >= 0x7f800000u;
-    const uint32_t e = lost ? uint32_t(kInt4ExpNaN) : int4_row_exponent(__uint_as_float(row_top));
-    const float down = lost ? 0.0f : __uint_as_float((254u - e) << 23);  // 2^(127 - e)
-    const uint32_t b = lost ? 127u : int4_scale_byte(__uint_as_float(top) * down);
+    const bool lost = !(row_top < INFINITY);
+    const uint32_t e = lost ? uint32_t(kInt4ExpNaN) : int4_row_exponent(row_top);
+    const uint32_t b = lost ? 127u : int4_scale_byte(top * __uint_as_float((254u - e) << 23));  // times 2^(127 - e)
     if (mine) {
-      const float s = int4_scale(b), reciprocal = 1.0f / s;
-      uint32_t w = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w |= (lost ? 8u : int4_code(x[i] * down, s, reciprocal)) << (4 * i);
-      reinterpret_cast<uint32_t*>(pool + row * (c.dim / 2))[lane] = int4_turned(w);
+      const float s = int4_scale(b) * __uint_as_float(e << 23);
+      reinterpret_cast<uint32_t*>(pool + row * (c.dim / 2))[lane] = int4_codes(x, s, e == kInt4ExpHigh);
     }
     // a byte of two lanes; those past the row's end fill its last word with zeros
     const int pitch = scale_pitch(c.dim), at = lane >> 1;
@@ -108,7 +145,7 @@ struct RawRow {
   __device__ __forceinline__ void load(const CacheDev& c, const uint8_t* pool, const uint8_t* exps, const uint8_t* scales,
                                        int64_t row, bool there, int lane) {
     w = make_uint4(0u, 0u, 0u, 0u);
-    exp = kExpBias;
+    exp = kRows == RowKind::kInt4 ? kInt4Zero : kExpBias;
     scale = 0u;
     if (!there) return;
     if constexpr (kRows == RowKind::kBf16) {
@@ -123,20 +160,45 @@ struct RawRow {
       scale = scales[row * scale_pitch(c.dim) + (lane >> 1)];
     }
   }
-  __device__ __forceinline__ void values(bool there, float (&v)[8]) const {
-    if constexpr (kRows == RowKind::kBf16) {
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
-    } else if constexpr (kRows == RowKind::kE4M3) {
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (kRows == RowKind::kE4M3) {
       values8(make_uint2(w.x, w.y), exp_value(exp), v);
-    } else {
-      const float unit = exp == kInt4ExpNaN ? __uint_as_float(0x7fc00000u)
-                                            : there ? int4_scale(scale) * exp_value(exp) : 0.0f;
-      const uint32_t u = int4_turned_back(w.x);
+      return;
+    }
+    if constexpr (kRows == RowKind::kInt4) bf16x8(u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)  // 2^23 + code
-        v[i] = (__uint_as_float((u >> (4 * i) & 15u) | 0x4b000000u) - (8388608.0f + 8.0f)) * unit;
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+  }
+  // INT4: the eight elements in bf16, which holds them exactly.
+  __device__ __forceinline__ void bf16x8(uint32_t (&u)[4]) const {
+    const uint32_t unit = int4_unit(scale, exp), minus = int4_minus_192(unit);
+    uint32_t r[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      int4_pair(w.x, j, 0x00780078u, 0x43004300u, r[2 * j], r[2 * j + 1]);
+      r[2 * j] = int4_fma(r[2 * j], unit, minus);
+      r[2 * j + 1] = int4_fma(r[2 * j + 1], unit, minus);
+    }
+    u[0] = __byte_perm(r[0], r[1], 0x5410);
+    u[1] = __byte_perm(r[2], r[3], 0x5410);
+    u[2] = __byte_perm(r[0], r[1], 0x7632);
+    u[3] = __byte_perm(r[2], r[3], 0x7632);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    float v[8];
+    values(v);
+    store_vec8(p, v);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    if constexpr (kRows == RowKind::kE4M3) {
+      float v[8];
+      values(v);
+      store_vec8(p, v);
+    } else {
+      uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      if constexpr (kRows == RowKind::kInt4) bf16x8(u);
+      *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     }
   }
 };

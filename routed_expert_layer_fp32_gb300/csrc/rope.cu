@@ -7,11 +7,13 @@
 // few thousand, and fp64 is slow on this GPU.  The top 32 bits are taken to the nearest quarter turn, and the rest,
 // within an eighth of a turn, to sincospi.
 //
-// What bounds it is memory: 6 operations a pair.  So a group of kLanes lanes takes a token, eight elements a lane of
-// each head, works out its elements' cosines and sines once and goes through the heads with them, the next head's
-// loads ahead of the current one's arithmetic.  Where pairs are half the turned part apart a lane loads its partners'
-// elements as well (they are in L1: another lane of the group loads them).  With few tokens the heads are shared out
-// over more groups: jobs of one head or more, queries first, then keys, then values.
+// What bounds it is memory: 6 operations a pair.  A group of kLanes lanes takes a token, eight elements of each head a
+// lane, works out its pairs' cosines and sines once and goes through heads with them, four heads' loads ahead of the
+// arithmetic.  Where the pairs are half the turned part apart, a lane has four elements of one half and their partners in
+// the other, so that nothing is read twice or exchanged, and a query may be turned in place.  Rows of the cache need
+// eight elements in a row (their scales and codes), so for keys and values a lane has those, and loads its keys' partners
+// as well (they are in L1: another lane of the group loads them).  The heads of a token are shared out over blocks: those
+// of the queries, then those of keys and values.
 #include "kv_rows.cuh"
 
 namespace moe {
@@ -94,11 +96,12 @@ __device__ __forceinline__ void turn_of(const RopeDev& r, int pos, int e0, bool 
 template <typename Src>
 struct Head {
   float x[8], y[8];
-  __device__ __forceinline__ void load(const Src* p, const Partners& with, bool mine) {
+  __device__ __forceinline__ void load(const Src* p, const Partners& with, bool turned, bool mine) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.0f;
     if (!mine) return;
     load_vec8(p, x);
+    if (!turned) return;
     if (with.by[0] == with.by[1]) {
       if (with.by[0] != 0 && (with.by[0] & 7) == 0) {
         load_vec8(p + with.by[0], y);
@@ -119,65 +122,158 @@ struct Head {
   }
 };
 
-// Heads [j0, j0 + each) of the list of q's, k's and v's heads, of one token a group.
-template <int kLanes, bool kCache, RowKind kRows, typename Src, typename Out>
-__global__ void __launch_bounds__(kThreads) k_rope(RopeArgs a, int each) {
-  const int t = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
-  const int e0 = lane * 8, all = a.q.heads + a.k.heads + a.v.heads;
-  const int j0 = blockIdx.y * each, j1 = min(all, j0 + each);
-  const bool here = t < a.T, mine = here && e0 < a.dim;
-  const Partners with(a.rope, e0);
-  pdl_begin();
-  const int pos = here ? __ldg(a.pos + t) : 0;
-  int64_t row0 = -1;  // of head 0 in the cache
-  if constexpr (kCache) {
-    if (here && j1 > a.q.heads) {
-      const int slot = __ldg(a.slot + t), page = unsigned(slot) / unsigned(a.cache.page);
-      if (slot >= 0) {
-        if (page < a.cache.n_pages) row0 = int64_t(page) * a.cache.heads * a.cache.page + (slot - page * a.cache.page);
-        else report_bad_page(a.status_flags);
+// Four elements as they lie.
+template <typename Src>
+struct Quad;
+template <>
+struct Quad<__nv_bfloat16> {
+  uint2 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void values(float (&x)[4]) const {
+    x[0] = __uint_as_float(u.x << 16), x[1] = __uint_as_float(u.x & 0xffff0000u);
+    x[2] = __uint_as_float(u.y << 16), x[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+};
+template <>
+struct Quad<float> {
+  float4 u;
+  __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void values(float (&x)[4]) const { x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w; }
+};
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+}
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+
+// Query heads [j0, j1) of token t.
+constexpr int kAhead = 4;
+template <typename Src, typename Out>
+__device__ __forceinline__ void turn_queries(const RopeArgs& a, int t, int lane, int j0, int j1) {
+  if (t >= a.T || lane * 8 >= a.dim) return;
+  const RopeDev& r = a.rope;
+  const bool turned = lane * 8 < r.dim, apart = turned && !r.interleaved;
+  const int e0 = apart ? 4 * lane : 8 * lane, e1 = apart ? r.dim / 2 + 4 * lane : 8 * lane + 4;
+  const Src* from = static_cast<const Src*>(a.q.x) + t * a.q.stride;
+  Out* to = static_cast<Out*>(a.out) + t * a.out_stride;
+  Quad<Src> next[kAhead][2];
+  auto fetch = [&](int j) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (j + i < j1) {
+        next[i][0].load(from + (j + i) * a.dim + e0);
+        next[i][1].load(from + (j + i) * a.dim + e1);
       }
+  };
+  fetch(j0);
+  float c[4], s[4];
+  const int pos = __ldg(a.pos + t);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 cs = turned ? cos_sin(__ldg(r.turns + 4 * lane + i), pos, r.magnitude) : make_float2(1.0f, 0.0f);
+    c[i] = cs.x;
+    s[i] = a.inverse ? -cs.y : cs.y;
+  }
+  for (int j = j0; j < j1; j += kAhead) {
+    Quad<Src> now[kAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) now[i][0] = next[i][0], now[i][1] = next[i][1];
+    fetch(j + kAhead);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (j + i >= j1) break;
+      float x[4], y[4];
+      now[i][0].values(x);
+      now[i][1].values(y);
+      if (apart) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float p = x[k], q = y[k];
+          x[k] = fmaf(p, c[k], -(q * s[k]));
+          y[k] = fmaf(q, c[k], p * s[k]);
+        }
+      } else if (turned) {
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const float p = x[k], q = x[k + 1], v = y[k], w = y[k + 1];
+          x[k] = fmaf(p, c[k / 2], -(q * s[k / 2]));
+          x[k + 1] = fmaf(q, c[k / 2], p * s[k / 2]);
+          y[k] = fmaf(v, c[2 + k / 2], -(w * s[2 + k / 2]));
+          y[k + 1] = fmaf(w, c[2 + k / 2], v * s[2 + k / 2]);
+        }
+      }
+      store4(to + (j + i) * a.dim + e0, x);
+      store4(to + (j + i) * a.dim + e1, y);
+    }
+  }
+}
+
+// Heads [j0, j1) of the list of keys' and then values' heads of token t, into the cache; the whole warp comes here.
+template <int kLanes, RowKind kRows, typename Src>
+__device__ __forceinline__ void place_rows(const RopeArgs& a, int t, int lane, int j0, int j1) {
+  const bool here = t < a.T, mine = here && lane * 8 < a.dim;
+  const int e0 = lane * 8;
+  const Partners with(a.rope, e0);
+  int64_t row0 = -1;  // of head 0
+  if (here) {
+    const int slot = __ldg(a.slot + t), page = unsigned(slot) / unsigned(a.cache.page);
+    if (slot >= 0) {
+      if (page < a.cache.n_pages) row0 = int64_t(page) * a.cache.heads * a.cache.page + (slot - page * a.cache.page);
+      else report_bad_page(a.status_flags);
     }
   }
   auto load = [&](int j, Head<Src>& h) {
-    const bool is_q = j < a.q.heads, is_k = !is_q && j < a.q.heads + a.k.heads;
-    const HeadRows& r = is_q ? a.q : is_k ? a.k : a.v;
-    const int head = is_q ? j : is_k ? j - a.q.heads : j - a.q.heads - a.k.heads;
-    h.load(static_cast<const Src*>(r.x) + t * r.stride + int64_t(head) * a.dim + e0, with, mine && j < j1);
+    const bool is_k = j < a.k.heads;
+    const HeadRows& r = is_k ? a.k : a.v;
+    h.load(static_cast<const Src*>(r.x) + t * r.stride + (is_k ? j : j - a.k.heads) * a.dim + e0, with, is_k,
+           mine && j < j1);
   };
   Head<Src> next;
   load(j0, next);
   Turn turn;
-  if (j0 < a.q.heads + a.k.heads) turn_of(a.rope, pos, mine ? e0 : a.rope.dim, a.inverse, turn);
+  if (j0 < a.k.heads) turn_of(a.rope, here ? __ldg(a.pos + t) : 0, mine ? e0 : a.rope.dim, a.inverse, turn);
   for (int j = j0; j < j1; ++j) {
     Head<Src> h = next;
     load(j + 1, next);
-    if (j < a.q.heads + a.k.heads) h.turn(turn, with);
-    if (!kCache || j < a.q.heads) {
-      __syncwarp();  // out may be x: the group's lanes have their partners' elements
-      if (mine) store_vec8(static_cast<Out*>(a.out) + t * a.out_stride + int64_t(j) * a.dim + e0, h.x);
-    } else if constexpr (kCache) {
-      const bool is_k = j < a.q.heads + a.k.heads;
-      const int head = j - a.q.heads - (is_k ? 0 : a.k.heads);
-      store_row<kLanes, kRows>(a.cache, is_k ? a.cache.k : a.cache.v, is_k ? a.cache.k_exp : a.cache.v_exp,
-                               is_k ? a.cache.k_scale : a.cache.v_scale, row0 + int64_t(head) * a.cache.page, row0 >= 0,
-                               lane, h.x);
-    }
+    const bool is_k = j < a.k.heads;
+    if (is_k) h.turn(turn, with);
+    store_row<kLanes, kRows>(a.cache, is_k ? a.cache.k : a.cache.v, is_k ? a.cache.k_exp : a.cache.v_exp,
+                             is_k ? a.cache.k_scale : a.cache.v_scale,
+                             row0 + int64_t(is_k ? j : j - a.k.heads) * a.cache.page, row0 >= 0, lane, h.x);
   }
 }
 
-// Heads a group: enough groups to fill the GPU, and with more tokens fewer that work out the same angles.
-int heads_each(int T, int heads, int lanes) {
-  const int64_t fill = int64_t(std::max(sm_count(), 1)) * 2048 / lanes;
-  return int(std::min<int64_t>(heads, std::max<int64_t>(1, int64_t(T) * heads / fill)));
+// Blocks [0, q_blocks) of the second axis take q_each query heads each, those behind them kv_each heads of keys and
+// values.
+template <int kLanes, bool kCache, RowKind kRows, typename Src, typename Out>
+__global__ void __launch_bounds__(kThreads) k_rope(RopeArgs a, int q_blocks, int q_each, int kv_each) {
+  const int t = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  pdl_begin();
+  if (!kCache || blockIdx.y < q_blocks) {
+    const int j0 = blockIdx.y * q_each;
+    turn_queries<Src, Out>(a, t, lane, j0, min(a.q.heads, j0 + q_each));
+  } else if constexpr (kCache) {
+    const int j0 = (blockIdx.y - q_blocks) * kv_each;
+    place_rows<kLanes, kRows, Src>(a, t, lane, j0, min(a.k.heads + a.v.heads, j0 + kv_each));
+  }
+}
+
+// Heads a block: as few as fill the GPU some times over; and not fewer than share the angles' cost where there are more
+// tokens than that.
+int heads_each(int T, int heads, int lanes, int enough) {
+  const int64_t groups = int64_t(std::max(sm_count(), 1)) * 1024 / lanes;
+  return int(std::min<int64_t>(std::min(heads, enough), std::max<int64_t>(1, int64_t(T) * heads / groups)));
 }
 
 template <int kLanes, bool kCache, RowKind kRows, typename Src, typename Out>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
-  const int heads = a.q.heads + a.k.heads + a.v.heads, each = heads_each(a.T, heads, kLanes);
-  const int tokens = kThreads / kLanes;
-  return launch_pdl(k_rope<kLanes, kCache, kRows, Src, Out>, dim3((a.T + tokens - 1) / tokens, (heads + each - 1) / each),
-                    dim3(kThreads), 0, s, a, each);
+  const int kv = a.k.heads + a.v.heads, q_each = heads_each(a.T, a.q.heads, kLanes, 8);
+  const int kv_each = kv > 0 ? heads_each(a.T, kv, kLanes, 4) : 1;
+  const int tokens = kThreads / kLanes, q_blocks = (a.q.heads + q_each - 1) / q_each;
+  return launch_pdl(k_rope<kLanes, kCache, kRows, Src, Out>,
+                    dim3((a.T + tokens - 1) / tokens, q_blocks + (kv + kv_each - 1) / kv_each), dim3(kThreads), 0, s, a,
+                    q_blocks, q_each, kv_each);
 }
 
 }  // namespace
