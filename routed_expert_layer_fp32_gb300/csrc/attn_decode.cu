@@ -98,8 +98,9 @@ struct Shape {
   static constexpr int kSpanElems = kDim / kSpans;
   // 32 KB stages (16 KB for the narrowest rows); 16 or 32 tokens a warp, those of one product with the
   // values
-  static constexpr int kPerWarp = kE4M3 || kInt4 ? 32 : 16;
-  static constexpr int kTokens = kRow <= 128 ? 128 : 128 * 128 / kRow;
+  static constexpr int kTokens = kInt4 && kRow <= 64 ? 256 : kRow <= 128 ? 128 : 128 * 128 / kRow;
+  static constexpr int kPerPass = kE4M3 || kInt4 ? 32 : 16;                   // tokens of one pass of a warp
+  static constexpr int kPerWarp = kInt4 && kTokens == 256 ? 64 : kPerPass;  // of a tile
   static constexpr int kGroupWarps = kTokens / kPerWarp;
   static constexpr int kGroups = kWarps / kGroupWarps;
   static constexpr int kTile = kTokens * kRow;
@@ -382,7 +383,7 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int row0, int box, uin
 // INT4: the values of the rows that a warp does not see made zeros by their scales and exponents (a lane a row).
 template <typename S>
 __device__ __forceinline__ void clear_scales(uint8_t* exps, int pitch, int row0, uint32_t seen, int lane) {
-  static_assert(!S::kInt4 || S::kPerWarp == 32, "a lane a row");
+  static_assert(!S::kInt4 || S::kPerPass == 32, "a lane a row");
   if (seen >> lane & 1) return;
   exps[S::kTokens + lane] = kInt4Zero;
   uint32_t* s = reinterpret_cast<uint32_t*>(exps - row0 + 2 * S::kTokens + S::kScales + (row0 + lane) * pitch);
@@ -627,7 +628,7 @@ struct Int4Operands {
 template <typename S>
 struct WarpBf16 {
   using Operands = std::conditional_t<S::kInt4, Int4Operands<S>, Bf16Operands<S>>;
-  static constexpr int kMT = S::kPerWarp / 16, kKS = S::kDim / 16, kNB = S::kHeads / 8;
+  static constexpr int kMT = S::kPerPass / 16, kKS = S::kDim / 16, kNB = S::kHeads / 8;
   uint32_t q[kKS][kNB][2];  // kQueriesStay: read where they are needed
   uint32_t queries_at;
   float m[kNB][2], sum[kNB][2], acc[kKS][kNB][4];
@@ -699,7 +700,7 @@ struct WarpBf16 {
         }
     }
     if constexpr (S::kInt4) {  // the masks are a part of the time here, and few tiles need them
-      if (tv.seen != 0xffffffffu >> (32 - S::kPerWarp)) {
+      if (tv.seen != 0xffffffffu >> (32 - S::kPerPass)) {
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
@@ -1397,26 +1398,28 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       for (int n = n0; n < walk.take; n += S::kGroups) {
         const int stage = (it + n) % S::kStages;
         if (!wait(&ctl->full[stage], ((it + n) / S::kStages) & 1, &ctl->abort)) timed_out = true;
-        tv.k = smem_u32(smem + size_t(stage) * S::kStage);
-        tv.v = tv.k + S::kTile;
-        tv.exps = exps + stage * S::kExps + row0;
-        tv.exps_at = smem_u32(tv.exps);
-        tv.scales_at = tv.exps_at - row0 + 2 * S::kTokens + row0 * pitch;
-        // the warp's tokens [from, to) of the tile lie in what is seen
-        const int pos0 = (walk.span.tile0 + walk.tile + n) * S::kTokens + row0;
-        const int from = max(0, walk.span.first - pos0), to = min(S::kPerWarp, walk.span.end - pos0);
-        constexpr uint32_t kAll = 0xffffffffu >> (32 - S::kPerWarp);
-        tv.seen = from < to ? kAll >> (S::kPerWarp - to + from) << from : 0u;
-        const uint32_t copied = ctl->valid[stage] >> (row0 / 16);
-        if (!(copied & 1)) tv.seen &= ~0xffffu;
-        if (S::kPerWarp == 32 && !(copied & 2)) tv.seen &= 0xffffu;
-        if (tv.seen != 0) {
+#pragma unroll 1
+        for (int row = row0; row < row0 + S::kPerWarp; row += S::kPerPass) {
+          tv.k = smem_u32(smem + size_t(stage) * S::kStage) + (row - row0) * S::kRow;
+          tv.v = tv.k + S::kTile;
+          tv.exps = exps + stage * S::kExps + row;
+          tv.exps_at = smem_u32(tv.exps);
+          tv.scales_at = tv.exps_at - row + 2 * S::kTokens + row * pitch;
+          // the warp's tokens [from, to) of the tile lie in what is seen
+          const int pos0 = (walk.span.tile0 + walk.tile + n) * S::kTokens + row;
+          const int from = max(0, walk.span.first - pos0), to = min(S::kPerPass, walk.span.end - pos0);
+          constexpr uint32_t kAll = 0xffffffffu >> (32 - S::kPerPass);
+          tv.seen = from < to ? kAll >> (S::kPerPass - to + from) << from : 0u;
+          const uint32_t copied = ctl->valid[stage] >> (row / 16);
+          if (!(copied & 1)) tv.seen &= ~0xffffu;
+          if (S::kPerPass == 32 && !(copied & 2)) tv.seen &= 0xffffu;
+          if (tv.seen == 0) continue;
           if (tv.seen != kAll) {
             if constexpr (S::kInt4) {
               // (written by cp.async, like these stores: no other proxy)
-              clear_scales<S>(exps + stage * S::kExps + row0, pitch, row0, tv.seen, lane);
+              clear_scales<S>(exps + stage * S::kExps + row, pitch, row, tv.seen, lane);
             } else {
-              clear_rows<S>(tv.v, row0, box, tv.seen, lane);
+              clear_rows<S>(tv.v, row, box, tv.seen, lane);
               fence_proxy_async_smem();  // before the next copy into these rows
             }
             __syncwarp();
