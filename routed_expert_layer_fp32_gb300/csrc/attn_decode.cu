@@ -63,9 +63,17 @@
 namespace moe {
 namespace {
 
-constexpr int kProducers = 2;    // start copies
-constexpr int kQueryWarps = 2;   // the second also zeroes the rows of empty sequences
-constexpr int kEndThreads = 128;  // end segments
+constexpr int kWarps = 8;      // compute
+constexpr int kProducers = 2;  // start copies
+constexpr int kQueryWarp = kWarps + kProducers;
+constexpr int kQueryWarps = 2;  // the second also zeroes the rows of empty sequences
+constexpr int kEndWarp = kWarps + 4;  // the first of those that end segments
+constexpr int kEndThreads = 128;
+constexpr int kThreads = kEndWarp * 32 + kEndThreads;
+// Registers a thread of the four warpgroups (compute twice, producers, segment ends); the launch gives
+// each 128, and the shares add up to that.
+constexpr int kComputeRegs = 160, kProducerRegs = 80, kEndRegs = 112;
+static_assert(2 * kComputeRegs + kProducerRegs + kEndRegs <= 4 * (65536 / kThreads), "registers");
 constexpr size_t kSmemLimit = 227 * 1024;
 constexpr int kMaxCtas = 256;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -77,19 +85,6 @@ template <RowKind kRows_, int kDim_, int kHeads_>
 struct Shape {
   static constexpr RowKind kRows = kRows_;
   static constexpr bool kE4M3 = kRows == RowKind::kE4M3, kInt4 = kRows == RowKind::kInt4;
-  // The warps: those that compute, then producers and queries, then those that end segments.  INT4 takes its codes apart
-  // in the computing warps and is bound by what they issue, so it has twelve where their registers allow.
-  static constexpr int kWarps = kInt4 && kDim_ * kHeads_ < 0 ? 12 : 8;
-  static constexpr int kQueryWarp = kWarps + kProducers;
-  static constexpr int kEndWarp = kQueryWarp + kQueryWarps;  // the first of those that end segments
-  static constexpr int kThreads = kEndWarp * 32 + kEndThreads;
-  // Registers a thread of the warpgroups (compute, producers and queries, segment ends); the launch gives each
-  // kLaunchRegs, and the shares add up to that.
-  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-  static constexpr int kComputeRegs = kWarps == 8 ? 160 : 104;
-  static constexpr int kProducerRegs = kWarps == 8 ? 80 : 80, kEndRegs = kWarps == 8 ? 112 : 88;
-  static constexpr bool kQueriesStay = kInt4;
-  static_assert(kWarps / 4 * kComputeRegs + kProducerRegs + kEndRegs <= kThreads / 128 * kLaunchRegs, "registers");
   static constexpr int kDim = kDim_;      // head_dim rounded up to 64, 128 or 256 (copies fill with zeros)
   static constexpr int kHeads = kHeads_;  // query heads of a segment
   static constexpr int kRow = kE4M3 ? kDim : kInt4 ? kDim / 2 : kDim * 2;  // bytes
@@ -99,7 +94,7 @@ struct Shape {
   // 32 KB stages (16 KB for the narrowest rows); 16 or 32 tokens a warp, those of one product with the
   // values
   static constexpr int kTokens = kInt4 && kRow <= 64 ? 256 : kRow <= 128 ? 128 : 128 * 128 / kRow;
-  static constexpr int kPerPass = kE4M3 || kInt4 ? 32 : 16;                   // tokens of one pass of a warp
+  static constexpr int kPerPass = kInt4 && kTokens == 256 ? 64 : kE4M3 || kInt4 ? 32 : 16;  // tokens of one pass of a warp
   static constexpr int kPerWarp = kInt4 && kTokens == 256 ? 64 : kPerPass;  // of a tile
   static constexpr int kGroupWarps = kTokens / kPerWarp;
   static constexpr int kGroups = kWarps / kGroupWarps;
@@ -338,6 +333,7 @@ struct TileView {
   uint32_t exps_at, scales_at;  // INT4: shared-memory addresses of them, and of the keys' scales; the values'
                                 // scales follow kScales further
   uint32_t seen;          // a bit for each of the warp's tokens
+  uint32_t seen_more;     // of the second 32
 };
 
 // Addresses for ldmatrix.  A tile lies in shared memory box by box (the tokens of one copy, a multiple
@@ -383,7 +379,6 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int row0, int box, uin
 // INT4: the values of the rows that a warp does not see made zeros by their scales and exponents (a lane a row).
 template <typename S>
 __device__ __forceinline__ void clear_scales(uint8_t* exps, int pitch, int row0, uint32_t seen, int lane) {
-  static_assert(!S::kInt4 || S::kPerPass == 32, "a lane a row");
   if (seen >> lane & 1) return;
   exps[S::kTokens + lane] = kInt4Zero;
   uint32_t* s = reinterpret_cast<uint32_t*>(exps - row0 + 2 * S::kTokens + S::kScales + (row0 + lane) * pitch);
@@ -629,8 +624,7 @@ template <typename S>
 struct WarpBf16 {
   using Operands = std::conditional_t<S::kInt4, Int4Operands<S>, Bf16Operands<S>>;
   static constexpr int kMT = S::kPerPass / 16, kKS = S::kDim / 16, kNB = S::kHeads / 8;
-  uint32_t q[kKS][kNB][2];  // kQueriesStay: read where they are needed
-  uint32_t queries_at;
+  uint32_t q[kKS][kNB][2];
   float m[kNB][2], sum[kNB][2], acc[kKS][kNB][4];
   float factor;  // scores to base-2 exponents
   Operands operands;
@@ -647,7 +641,6 @@ struct WarpBf16 {
 
   __device__ __forceinline__ void begin(const uint8_t* queries, int lane) {
     factor = *reinterpret_cast<const float*>(queries + S::kQueryRegs * 128);
-    queries_at = smem_u32(queries) + lane * 16;
 #pragma unroll
     for (int nb = 0; nb < kNB; ++nb) {
       m[nb][0] = m[nb][1] = -INFINITY;
@@ -657,7 +650,7 @@ struct WarpBf16 {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[ks][nb][i] = 0.0f;
 #pragma unroll
-      for (int ks = 0; ks < kKS && !S::kQueriesStay; ks += 2) {
+      for (int ks = 0; ks < kKS; ks += 2) {
         const uint4 u = *reinterpret_cast<const uint4*>(queries + ((nb * kKS + ks) / 2 * 32 + lane) * 16);
         q[ks][nb][0] = u.x, q[ks][nb][1] = u.y, q[ks + 1][nb][0] = u.z, q[ks + 1][nb][1] = u.w;
       }
@@ -677,15 +670,6 @@ struct WarpBf16 {
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         uint32_t r[4];
-        if constexpr (S::kQueriesStay) {
-          if (ks % 2 == 0)
-#pragma unroll
-            for (int nb = 0; nb < kNB; ++nb)
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(q[ks][nb][0]), "=r"(q[ks][nb][1]), "=r"(q[ks + 1][nb][0]), "=r"(q[ks + 1][nb][1])
-                           : "r"(queries_at + (nb * kKS + ks) / 2 * 512)
-                           : "memory");
-        }
         operands.key(tv, mt, ks, r);
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb) mma_bf16_16x8x16(ks & 1 ? s2[nb] : s[mt][nb], r, q[ks][nb][0], q[ks][nb][1]);
@@ -700,14 +684,14 @@ struct WarpBf16 {
         }
     }
     if constexpr (S::kInt4) {  // the masks are a part of the time here, and few tiles need them
-      if (tv.seen != 0xffffffffu >> (32 - S::kPerPass)) {
+      if ((S::kPerPass == 64 ? tv.seen & tv.seen_more : tv.seen) != 0xffffffffu) {
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
           for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (!(seen >> (mt * 16 + (i >> 1) * 8) & 1)) s[mt][nb][i] = -INFINITY;
+              if (!((mt < 2 ? seen : tv.seen_more >> g) >> (mt % 2 * 16 + (i >> 1) * 8) & 1)) s[mt][nb][i] = -INFINITY;
       }
     }
     float base[kNB][2], fix[kNB][2];
@@ -1154,7 +1138,7 @@ __device__ __forceinline__ void for_constants(std::integer_sequence<int, I...>, 
 }
 
 template <typename S>
-__global__ void __launch_bounds__(S::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     k_attn_decode(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   int box, int copies, int page_boxes, uint32_t page_magic, int group, int head_blocks) {
   using Control = typename S::Control;
@@ -1177,7 +1161,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     }
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&ctl->q_full[i], 1);
-      mbar_init(&ctl->q_empty[i], S::kWarps);
+      mbar_init(&ctl->q_empty[i], kWarps);
     }
     for (int i = 0; i < S::kGroups; ++i) {
       mbar_init(&ctl->join_full[i], S::kGroupWarps);
@@ -1191,7 +1175,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   }
   // What a producer warp needs that no earlier kernel writes: lane's copy of every tile (one of keys or
   // values, one span or all, one box).
-  const int me = warp - S::kWarps;
+  const int me = warp - kWarps;
   const int boxes = S::kTokens / box;    // of a tile: 1, 2, 4 or 8
   const int box_shift = __ffs(2 * copies) - 1, row_shift = __ffs(box) - 1;
   const uint32_t job_bytes = uint32_t(box * S::kRow) >> (box_shift - 1);
@@ -1212,7 +1196,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   pdl_begin();
 
   // The line's length and the place where this CTA's part begins.
-  const int per = (a.B + S::kThreads - 1) / S::kThreads;
+  const int per = (a.B + kThreads - 1) / kThreads;
   const int b_lo = min(a.B, int(threadIdx.x) * per), b_hi = min(a.B, b_lo + per);
   int mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
@@ -1229,7 +1213,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   __syncthreads();
   int total = 0;
 #pragma unroll
-  for (int w = 0; w < S::kThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w == warp) upto += total;
     total += ctl->scan[w];
   }
@@ -1257,9 +1241,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   walk.start(a, ctl->b0, ctl->off0, lo, hi);
   int it = 0, seg = 0;
 
-  if (warp >= S::kWarps && warp < S::kEndWarp) {
-    fewer_registers<S::kProducerRegs>();
-    if (warp < S::kQueryWarp) {
+  if (warp >= kWarps && warp < kEndWarp) {
+    fewer_registers<kProducerRegs>();
+    if (warp < kQueryWarp) {
       // --------------------------------------------------------------- producers ------------
       bool ok = true;
       for (; ok && !walk.done(); walk.next(a, segs)) {
@@ -1347,7 +1331,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
       }
     } else {
-      if (warp == S::kQueryWarp + 1) {
+      if (warp == kQueryWarp + 1) {
         // ----------------------------------------- sequences without a token: zeros ---------
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
           if (span_of<S>(a, b).tiles != 0) continue;
@@ -1360,7 +1344,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       // ------------------------------- queries, the segments in turn by the two warps -------
       for (; !walk.done(); walk.next(a, segs), ++seg) {
-        if (seg % kQueryWarps != warp - S::kQueryWarp) continue;
+        if (seg % kQueryWarps != warp - kQueryWarp) continue;
         const int kv = walk.kv(head_blocks), hb = walk.seg - kv * head_blocks, slot = seg % S::kSlots;
         if (!__all_sync(0xffffffffu, wait_part(&ctl->q_empty[slot], ((seg / S::kSlots) & 1) ^ 1, &ctl->abort))) {
           if (lane == 0) report_timeout_flag(a.table.status_flags, 41);
@@ -1376,23 +1360,21 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     return;
   }
 
-  if (warp < S::kWarps) {
+  if (warp < kWarps) {
     // ------------------------------------------------------------------ compute -------------
-    more_registers<S::kComputeRegs>();
+    more_registers<kComputeRegs>();
     const int wg = warp / S::kGroupWarps, row0 = (warp % S::kGroupWarps) * S::kPerWarp;
     bool timed_out = false;
     int joins = 0;  // the group's passes through the join buffer so far
     Compute mine_w(row0, lane, box, c.dim);
     for (; !walk.done(); it += walk.take, walk.next(a, segs), ++seg) {
       const int hb = walk.seg - walk.kv(head_blocks) * head_blocks, slot = seg % S::kSlots;
-      const int n0 = unsigned(wg + S::kGroups - it % S::kGroups) % S::kGroups;  // the group's first tile of the segment
+      const int n0 = unsigned(wg - it) % S::kGroups;  // the group's first tile of the segment
       if (!wait(&ctl->q_full[slot], (seg / S::kSlots) & 1, &ctl->abort)) timed_out = true;
       // (under a condition, n0 < walk.take, more registers spill: 16 heads, 64 x 8k bf16 68.1 us against 66.5)
       mine_w.begin(queries + slot * S::kQueries, lane);
-      if (!S::kQueriesStay || n0 >= walk.take) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->q_empty[slot]);
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_empty[slot]);
       if (n0 >= walk.take) continue;
       TileView tv;
       for (int n = n0; n < walk.take; n += S::kGroups) {
@@ -1405,19 +1387,27 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           tv.exps = exps + stage * S::kExps + row;
           tv.exps_at = smem_u32(tv.exps);
           tv.scales_at = tv.exps_at - row + 2 * S::kTokens + row * pitch;
-          // the warp's tokens [from, to) of the tile lie in what is seen
+          // the warp's tokens of the tile that lie in what is seen
           const int pos0 = (walk.span.tile0 + walk.tile + n) * S::kTokens + row;
-          const int from = max(0, walk.span.first - pos0), to = min(S::kPerPass, walk.span.end - pos0);
-          constexpr uint32_t kAll = 0xffffffffu >> (32 - S::kPerPass);
-          tv.seen = from < to ? kAll >> (S::kPerPass - to + from) << from : 0u;
-          const uint32_t copied = ctl->valid[stage] >> (row / 16);
-          if (!(copied & 1)) tv.seen &= ~0xffffu;
-          if (S::kPerPass == 32 && !(copied & 2)) tv.seen &= 0xffffu;
-          if (tv.seen == 0) continue;
-          if (tv.seen != kAll) {
+          constexpr int kWord = S::kPerPass < 32 ? S::kPerPass : 32;
+          constexpr uint32_t kAll = 0xffffffffu >> (32 - kWord);
+          auto seen_of = [&](int at) {  // [from, to) of kWord tokens
+            const int from = max(0, walk.span.first - pos0 - at), to = min(kWord, walk.span.end - pos0 - at);
+            uint32_t bits = from < to ? kAll >> (kWord - to + from) << from : 0u;
+            const uint32_t copied = ctl->valid[stage] >> ((row + at) / 16);
+            if (!(copied & 1)) bits &= ~0xffffu;
+            if (kWord == 32 && !(copied & 2)) bits &= 0xffffu;
+            return bits;
+          };
+          tv.seen = seen_of(0);
+          tv.seen_more = S::kPerPass == 64 ? seen_of(32) : 0u;
+          if ((tv.seen | tv.seen_more) == 0) continue;
+          if (tv.seen != kAll || (S::kPerPass == 64 && tv.seen_more != kAll)) {
             if constexpr (S::kInt4) {
               // (written by cp.async, like these stores: no other proxy)
               clear_scales<S>(exps + stage * S::kExps + row, pitch, row, tv.seen, lane);
+              if constexpr (S::kPerPass == 64)
+                clear_scales<S>(exps + stage * S::kExps + row + 32, pitch, row + 32, tv.seen_more, lane);
             } else {
               clear_rows<S>(tv.v, row, box, tv.seen, lane);
               fence_proxy_async_smem();  // before the next copy into these rows
@@ -1429,7 +1419,6 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->empty[stage]);
       }
-      if (S::kQueriesStay && lane == 0) mbar_arrive(&ctl->q_empty[slot]);
       const int heads = min(S::kHeads, group - hb * S::kHeads);
       for_constants(std::make_integer_sequence<int, S::kPasses>{}, [&](auto pass) {
         constexpr int kPass = decltype(pass)::value;
@@ -1447,8 +1436,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   }
 
   // ---------------------------------------------------------------------- segment ends ------
-  fewer_registers<S::kEndRegs>();
-  const int tid = threadIdx.x - S::kEndWarp * 32;
+  fewer_registers<kEndRegs>();
+  const int tid = threadIdx.x - kEndWarp * 32;
   bool timed_out = false;
   int n_joints = 0;
   uint32_t phases = 0;  // a bit for each group: the parity of its next pass through the join buffer
@@ -1487,10 +1476,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         };
         if (groups == (1u << S::kGroups) - 1) {
 #pragma unroll
-          for (int w = 0; w < S::kWarps; ++w) top_of(w);
+          for (int w = 0; w < kWarps; ++w) top_of(w);
           const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-          for (int w = 0; w < S::kWarps; ++w) add(w, base);
+          for (int w = 0; w < kWarps; ++w) add(w, base);
         } else {
           for (uint32_t left = groups; left; left &= left - 1)
 #pragma unroll
@@ -1587,7 +1576,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     cudaFuncAttributes f;
     attr = cudaFuncGetAttributes(&f, k_attn_decode<S>);
     // the warpgroups divide up what the launch gets: with less than they ask for they would wait for ever
-    if (attr == cudaSuccess && S::kThreads / 128 * f.numRegs < S::kWarps / 4 * S::kComputeRegs + S::kProducerRegs + S::kEndRegs)
+    if (attr == cudaSuccess && 4 * f.numRegs < 2 * kComputeRegs + kProducerRegs + kEndRegs)
       attr = cudaErrorInvalidConfiguration;
     if (attr == cudaSuccess)
       attr = cudaFuncSetAttribute(k_attn_decode<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(S::kSmem));
@@ -1606,7 +1595,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
   // i / page_boxes = the high half of i * page_magic, for i below 2^32 / page_boxes: positions below 2^28
   // make at most 2^24 boxes of 16, and a page at most 256
   const uint32_t page_magic = uint32_t(((uint64_t(1) << 32) + page_boxes - 1) / page_boxes);
-  return launch_pdl(k_attn_decode<S>, dim3(ctas), dim3(S::kThreads), S::kSmem, s, a, mk, mv, box,
+  return launch_pdl(k_attn_decode<S>, dim3(ctas), dim3(kThreads), S::kSmem, s, a, mk, mv, box,
                     S::kSpans / spans, page_boxes, page_magic, group, (group + S::kHeads - 1) / S::kHeads);
 }
 

@@ -44,6 +44,8 @@ __device__ __forceinline__ void values8(uint2 codes, float unit, float (&v)[8]) 
   }
 }
 
+__constant__ const float kReciprocals[8] = {1.0f, 8.0f / 9, 8.0f / 10, 8.0f / 11, 8.0f / 12, 8.0f / 13, 8.0f / 14, 8.0f / 15};
+
 // The largest of magnitudes, NaN where one of them is (fmaxf would leave it out).
 __device__ __forceinline__ float max_or_nan(float a, float b) {
   float r;
@@ -51,23 +53,21 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
   return r;
 }
 
-// The codes of eight elements, x_i / s to the nearest whole number of -7 .. 7, ties to even, plus 8, in the order of the
-// cache (s the scale times the row's power of two, which changes no rounding here).  With the reciprocal rounded to
+// The codes of eight elements of magnitude up to 7 s, x_i / s to the nearest whole number, ties to even, plus 8, in the
+// order of the cache (s the scale times the row's power of two, which changes no rounding here).  With the reciprocal rounded to
 // nearest, the quotient put right by its remainder (exact, by a fused multiply-add) is the correctly rounded one
 // [Markstein 1990]; and that lies on the same side of a border k + 1/2 as the exact one, or on it with it: a border
 // times s has 7 bits, and the next fp32 number is further from it than the quotient's rounding reaches.  Added to
 // 1.5 * 2^23 + 8 it is rounded to a whole number, whose code stands in the low bits; multiply-adds put the eight side by
 // side, and what is above the low bits adds up to a constant.
-__device__ __forceinline__ uint32_t int4_codes(const float (&x)[8], float s, bool cut) {
+__device__ __forceinline__ uint32_t int4_codes(const float (&x)[8], float s, float reciprocal) {
   constexpr float kWhole = 12582912.0f + 8.0f;
   constexpr uint32_t kAbove = 0x4b400000u;  // 1.5 * 2^23's bits
-  const float reciprocal = __frcp_rn(s);
   uint32_t w = 0u - kAbove * 0x11111111u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float q = x[i] * reciprocal;
-    float n = fmaf(fmaf(-q, s, x[i]), reciprocal, q);
-    if (cut) n = fminf(fmaxf(n, -kInt4Most), kInt4Most);
+    const float n = fmaf(fmaf(-q, s, x[i]), reciprocal, q);
     w += __float_as_uint(n + kWhole) << (4 * i);
   }
   return (w << 3 & 0xfff8fff8u) | (w >> 13 & 0x00070007u);
@@ -105,7 +105,7 @@ __device__ __forceinline__ uint32_t int4_unit(uint32_t scale, uint32_t exp) {
 // lane's eight elements, zeros past the row's end.
 template <int kLanes, RowKind kRows>
 __device__ __forceinline__ void store_row(const CacheDev& c, uint8_t* pool, uint8_t* exps, uint8_t* scales, int64_t row,
-                                          bool write, int lane, const float (&x)[8]) {
+                                          bool write, int lane, float (&x)[8]) {
   const bool mine = lane * 8 < c.dim;
   if constexpr (kRows == RowKind::kBf16) {
     if (write && mine) store_vec8(reinterpret_cast<__nv_bfloat16*>(pool) + row * c.dim + lane * 8, x);
@@ -128,7 +128,14 @@ __device__ __forceinline__ void store_row(const CacheDev& c, uint8_t* pool, uint
     const uint32_t b = lost ? 127u : int4_scale_byte(top * __uint_as_float((254u - e) << 23));  // times 2^(127 - e)
     if (mine) {
       const float s = int4_scale(b) * __uint_as_float(e << 23);
-      reinterpret_cast<uint32_t*>(pool + row * (c.dim / 2))[lane] = int4_codes(x, s, e == kInt4ExpHigh);
+      // of the eight mantissas a scale has, each rounded to nearest, times powers of two
+      const float reciprocal =
+          kReciprocals[b & 7] * (__uint_as_float((139u - (b >> 3)) << 23) * __uint_as_float((254u - e) << 23));
+      if (__builtin_expect(e == kInt4ExpHigh, 0)) {  // magnitudes past 7 s
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -kInt4Most * s), kInt4Most * s);
+      }
+      reinterpret_cast<uint32_t*>(pool + row * (c.dim / 2))[lane] = int4_codes(x, s, reciprocal);
     }
     // a byte of two lanes; those past the row's end fill its last word with zeros
     const int pitch = scale_pitch(c.dim), at = lane >> 1;
