@@ -81,7 +81,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMinExp = -100;  // least value exponent that enters m: keeps the sum inside fp32's range
 static_assert(kMaxCtas <= kAttnTickets, "a counter a CTA");
 
-template <RowKind kRows_, int kDim_, int kHeads_>
+template <RowKind kRows_, int kDim_, int kHeads_, bool kShort = false>
 struct Shape {
   static constexpr RowKind kRows = kRows_;
   static constexpr bool kE4M3 = kRows == RowKind::kE4M3, kInt4 = kRows == RowKind::kInt4;
@@ -92,10 +92,14 @@ struct Shape {
   static constexpr int kSpans = kRow / kSpan;
   static constexpr int kSpanElems = kDim / kSpans;
   // 32 KB stages (16 KB for the narrowest rows); 16 or 32 tokens a warp, those of one product with the
-  // values
-  static constexpr int kTokens = kInt4 && kRow <= 64 ? 256 : kRow <= 128 ? 128 : 128 * 128 / kRow;
-  static constexpr int kPerPass = kInt4 && kTokens == 256 ? 64 : kE4M3 || kInt4 ? 32 : 16;  // tokens of one pass of a warp
-  static constexpr int kPerWarp = kInt4 && kTokens == 256 ? 64 : kPerPass;  // of a tile
+  // values (INT4: 32 or 64)
+  // INT4: stages of half the bytes up to 128 wide, but 256 tokens, as the producers' work a tile is most of a tile's time
+  // with fewer (64 x 16k tokens, 8 heads a kv head: 90 us, with 128 tokens 105); 64 of them a warp where the registers
+  // hold their scores.  With 128 tokens where segments are short, as more warps then share one (128
+  // windows of 513: 23.3 us against 27.4; 177 sequences of up to 42: 19.4 against 25.8).
+  static constexpr bool kWide = kInt4 && kRow <= 64 && !kShort;
+  static constexpr int kTokens = kWide ? 256 : kRow <= 128 ? 128 : 128 * 128 / kRow;
+  static constexpr int kPerWarp = kWide && kHeads == 8 ? 64 : kE4M3 || kInt4 ? 32 : 16;
   static constexpr int kGroupWarps = kTokens / kPerWarp;
   static constexpr int kGroups = kWarps / kGroupWarps;
   static constexpr int kTile = kTokens * kRow;
@@ -376,12 +380,13 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int row0, int box, uin
   }
 }
 
-// INT4: the values of the rows that a warp does not see made zeros by their scales and exponents (a lane a row).
+// INT4: the values of rows row0 .. row0 + 31 of a tile that are not seen made zeros by their scales and exponents, a
+// lane a row.
 template <typename S>
 __device__ __forceinline__ void clear_scales(uint8_t* exps, int pitch, int row0, uint32_t seen, int lane) {
   if (seen >> lane & 1) return;
-  exps[S::kTokens + lane] = kInt4Zero;
-  uint32_t* s = reinterpret_cast<uint32_t*>(exps - row0 + 2 * S::kTokens + S::kScales + (row0 + lane) * pitch);
+  exps[S::kTokens + row0 + lane] = kInt4Zero;
+  uint32_t* s = reinterpret_cast<uint32_t*>(exps + 2 * S::kTokens + S::kScales + (row0 + lane) * pitch);
   for (int w = 0; w < pitch / 4; ++w) s[w] = 0u;
 }
 
@@ -623,7 +628,7 @@ struct Int4Operands {
 template <typename S>
 struct WarpBf16 {
   using Operands = std::conditional_t<S::kInt4, Int4Operands<S>, Bf16Operands<S>>;
-  static constexpr int kMT = S::kPerPass / 16, kKS = S::kDim / 16, kNB = S::kHeads / 8;
+  static constexpr int kMT = S::kPerWarp / 16, kKS = S::kDim / 16, kNB = S::kHeads / 8;
   uint32_t q[kKS][kNB][2];
   float m[kNB][2], sum[kNB][2], acc[kKS][kNB][4];
   float factor;  // scores to base-2 exponents
@@ -684,7 +689,7 @@ struct WarpBf16 {
         }
     }
     if constexpr (S::kInt4) {  // the masks are a part of the time here, and few tiles need them
-      if ((S::kPerPass == 64 ? tv.seen & tv.seen_more : tv.seen) != 0xffffffffu) {
+      if ((S::kPerWarp == 64 ? tv.seen & tv.seen_more : tv.seen) != 0xffffffffu) {
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
@@ -1380,36 +1385,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = n0; n < walk.take; n += S::kGroups) {
         const int stage = (it + n) % S::kStages;
         if (!wait(&ctl->full[stage], ((it + n) / S::kStages) & 1, &ctl->abort)) timed_out = true;
-#pragma unroll 1
-        for (int row = row0; row < row0 + S::kPerWarp; row += S::kPerPass) {
-          tv.k = smem_u32(smem + size_t(stage) * S::kStage) + (row - row0) * S::kRow;
-          tv.v = tv.k + S::kTile;
-          tv.exps = exps + stage * S::kExps + row;
-          tv.exps_at = smem_u32(tv.exps);
-          tv.scales_at = tv.exps_at - row + 2 * S::kTokens + row * pitch;
-          // the warp's tokens of the tile that lie in what is seen
-          const int pos0 = (walk.span.tile0 + walk.tile + n) * S::kTokens + row;
-          constexpr int kWord = S::kPerPass < 32 ? S::kPerPass : 32;
-          constexpr uint32_t kAll = 0xffffffffu >> (32 - kWord);
-          auto seen_of = [&](int at) {  // [from, to) of kWord tokens
-            const int from = max(0, walk.span.first - pos0 - at), to = min(kWord, walk.span.end - pos0 - at);
-            uint32_t bits = from < to ? kAll >> (kWord - to + from) << from : 0u;
-            const uint32_t copied = ctl->valid[stage] >> ((row + at) / 16);
-            if (!(copied & 1)) bits &= ~0xffffu;
-            if (kWord == 32 && !(copied & 2)) bits &= 0xffffu;
-            return bits;
-          };
-          tv.seen = seen_of(0);
-          tv.seen_more = S::kPerPass == 64 ? seen_of(32) : 0u;
-          if ((tv.seen | tv.seen_more) == 0) continue;
-          if (tv.seen != kAll || (S::kPerPass == 64 && tv.seen_more != kAll)) {
+        tv.k = smem_u32(smem + size_t(stage) * S::kStage);
+        tv.v = tv.k + S::kTile;
+        tv.exps = exps + stage * S::kExps + row0;
+        tv.exps_at = smem_u32(tv.exps);
+        tv.scales_at = tv.exps_at - row0 + 2 * S::kTokens + row0 * pitch;
+        // the warp's tokens of the tile that lie in what is seen
+        const int pos0 = (walk.span.tile0 + walk.tile + n) * S::kTokens + row0;
+        constexpr int kWord = S::kPerWarp < 32 ? S::kPerWarp : 32;
+        constexpr uint32_t kAll = 0xffffffffu >> (32 - kWord);
+        auto seen_of = [&](int at) {  // [from, to) of kWord tokens
+          const int from = max(0, walk.span.first - pos0 - at), to = min(kWord, walk.span.end - pos0 - at);
+          uint32_t bits = from < to ? kAll >> (kWord - to + from) << from : 0u;
+          const uint32_t copied = ctl->valid[stage] >> ((row0 + at) / 16);
+          if (!(copied & 1)) bits &= ~0xffffu;
+          if (kWord == 32 && !(copied & 2)) bits &= 0xffffu;
+          return bits;
+        };
+        tv.seen = seen_of(0);
+        tv.seen_more = S::kPerWarp == 64 ? seen_of(32) : 0u;
+        if ((tv.seen | tv.seen_more) != 0) {
+          if (tv.seen != kAll || (S::kPerWarp == 64 && tv.seen_more != kAll)) {
             if constexpr (S::kInt4) {
               // (written by cp.async, like these stores: no other proxy)
-              clear_scales<S>(exps + stage * S::kExps + row, pitch, row, tv.seen, lane);
-              if constexpr (S::kPerPass == 64)
-                clear_scales<S>(exps + stage * S::kExps + row + 32, pitch, row + 32, tv.seen_more, lane);
+              uint8_t* const e = exps + stage * S::kExps;
+              clear_scales<S>(e, pitch, row0, tv.seen, lane);
+              if constexpr (S::kPerWarp == 64) clear_scales<S>(e, pitch, row0 + 32, tv.seen_more, lane);
             } else {
-              clear_rows<S>(tv.v, row, box, tv.seen, lane);
+              clear_rows<S>(tv.v, row0, box, tv.seen, lane);
               fence_proxy_async_smem();  // before the next copy into these rows
             }
             __syncwarp();
@@ -1605,16 +1608,26 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 //   is the joint of the partial results, lose: 8 x 8k 21 against 16), 8 at widths above 128.
 //   E4M3: up to 8 (16 spill: 29.3 us against 16.7 in two passes; a group of 8 in one pass 70 us, in two of
 //   4 108), 4 at widths above 128 (8 spill: 39.0 against 28.6).
+//   INT4: as bf16, which its products are; and with shorter tiles where no segment can be longer than kShortSegment.
+constexpr int kShortSegment = 1024;
 template <typename F>
-auto with_shape(const CacheDev& c, int group, F f) {
+auto with_shape(const CacheDev& c, int group, int longest, F f) {
   if (c.rows == RowKind::kE4M3) {
     if (c.dim <= 64) return group <= 4 ? f(Shape<RowKind::kE4M3, 64, 4>{}) : f(Shape<RowKind::kE4M3, 64, 8>{});
     if (c.dim <= 128) return group <= 4 ? f(Shape<RowKind::kE4M3, 128, 4>{}) : f(Shape<RowKind::kE4M3, 128, 8>{});
     return f(Shape<RowKind::kE4M3, 256, 4>{});
   }
   if (c.rows == RowKind::kInt4) {
-    if (c.dim <= 64) return group <= 8 ? f(Shape<RowKind::kInt4, 64, 8>{}) : f(Shape<RowKind::kInt4, 64, 16>{});
-    if (c.dim <= 128) return group <= 8 ? f(Shape<RowKind::kInt4, 128, 8>{}) : f(Shape<RowKind::kInt4, 128, 16>{});
+    auto of = [&](auto dim, auto heads) {
+      constexpr int D = decltype(dim)::value, H = decltype(heads)::value;
+      return longest <= kShortSegment ? f(Shape<RowKind::kInt4, D, H, true>{}) : f(Shape<RowKind::kInt4, D, H>{});
+    };
+    std::integral_constant<int, 64> d64;
+    std::integral_constant<int, 128> d128;
+    std::integral_constant<int, 8> h8;
+    std::integral_constant<int, 16> h16;
+    if (c.dim <= 64) return group <= 8 ? of(d64, h8) : of(d64, h16);
+    if (c.dim <= 128) return group <= 8 ? of(d128, h8) : of(d128, h16);
     return f(Shape<RowKind::kInt4, 256, 8>{});
   }
   if (c.dim <= 64) return group <= 8 ? f(Shape<RowKind::kBf16, 64, 8>{}) : f(Shape<RowKind::kBf16, 64, 16>{});
@@ -1625,13 +1638,15 @@ auto with_shape(const CacheDev& c, int group, F f) {
 }  // namespace
 
 size_t attn_workspace_bytes(const CacheDev& c, int n_heads, int) {
-  return kAttnPartialsAt + with_shape(c, n_heads / c.heads, [](auto shape) {
+  return kAttnPartialsAt + with_shape(c, n_heads / c.heads, 0, [](auto shape) {  // (partial results are alike for any length)
            return size_t(kMaxCtas) * 2 * decltype(shape)::kSlot * sizeof(float);
          });
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
-  return with_shape(a.cache, a.n_heads / a.cache.heads, [&](auto shape) { return launch<decltype(shape)>(a, s); });
+  const int room = a.table.max_pages * a.cache.page, longest = a.window > 0 ? std::min(a.window, room) : room;
+  return with_shape(a.cache, a.n_heads / a.cache.heads, longest,
+                    [&](auto shape) { return launch<decltype(shape)>(a, s); });
 }
 
 }  // namespace moe
