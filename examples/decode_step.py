@@ -6,10 +6,14 @@ then the expert layer, on one bf16 residual stream.
 
 The two projections are plain library products.  Four of five layers see a sliding window of 513
 tokens, every fifth the whole context ("We Ported Aleph Alpha's Kolibri to a MacBook. Our Own Gate
-Said No.", section "The gate"; it gives no head counts, and the rotation of the windowed layers' queries
-and keys is the caller's, between the projection and kv_write).  Weights are random.
+Said No.", section "The gate"; it gives no head counts, and says nothing of how the windowed layers'
+queries and keys are turned).  Weights are random.
 
-    python examples/decode_step.py [--batch 64] [--context 4096] [--layers 5] [--steps 50] [--cache e4m3]
+With --serve the pages come from a pool that the sequences share: each step plans its tokens' places on the GPU
+(page_plan), the windowed layers turn queries and keys on the way into the cache (rope_kv_write), and sequences that
+have ended give their pages back (page_release); all of a step is in one CUDA graph, pages that it hands out included.
+
+    python examples/decode_step.py [--batch 64] [--context 4096] [--layers 5] [--steps 50] [--cache e4m3] [--serve]
 """
 from __future__ import annotations
 
@@ -22,7 +26,7 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import routed_expert_layer_fp32_gb300 as moe  # noqa: E402
-from routed_expert_layer_fp32_gb300.binding import MOE_BF16, MOE_E4M3  # noqa: E402
+from routed_expert_layer_fp32_gb300.binding import MOE_BF16, MOE_E4M3, MOE_INT4  # noqa: E402
 
 WINDOW, FULL_EVERY = 513, 5
 
@@ -67,27 +71,73 @@ class Decoder:
         self.attn_ws = moe.attn_workspace(blocks[0].cache, heads, batch)
         self.moe_ws = moe.workspace(blocks[0].experts, batch)
 
+    def place(self, b, q, k, v):
+        """k and v of this step's tokens into the block's cache; the queries that attend to it."""
+        moe.kv_write(k, v, b.cache, self.pos, self.page_table, self.attn_ws)
+        return q
+
     def step(self):
         h, hk, dim, batch = self.heads, self.kv_heads, self.dim, self.residual.shape[0]
         rows = self.qkv.view(batch, h + 2 * hk, dim)
         moe.block_norm(self.residual, self.blocks[0].attn_norm, out=self.x)
         for i, b in enumerate(self.blocks):
             torch.mm(self.x, b.w_qkv, out=self.qkv)
-            moe.kv_write(rows[:, h:h + hk], rows[:, h + hk:], b.cache, self.pos, self.page_table, self.attn_ws)
-            moe.attn_decode(rows[:, :h], b.cache, self.lens, self.page_table, self.attn_ws, window=b.window, out=self.attn)
+            q = self.place(b, rows[:, :h], rows[:, h:h + hk], rows[:, h + hk:])
+            moe.attn_decode(q, b.cache, self.lens, self.page_table, self.attn_ws, window=b.window, out=self.attn)
             torch.mm(self.attn.view(batch, -1), b.w_out, out=self.proj)
             moe.block_norm(self.residual, b.moe_norm, y=self.proj, out=self.x)
             moe.forward(self.x, b.experts, self.moe_ws, out=self.y, ids=self.ids[i], w=self.wts)
             following = self.blocks[i + 1].attn_norm if i + 1 < len(self.blocks) else None
             moe.block_norm(self.residual, following, y=self.y, w_post=b.moe_post_norm, alpha=self.alpha,
                            out=None if following is None else self.x)
+        self.advance()
+        return self.residual
+
+    def advance(self):
         self.pos += 1
         self.lens += 1
-        return self.residual
+
+
+class Server(Decoder):
+    """A Decoder whose sequences share a pool of pages and whose windowed layers turn queries and keys.  `lens` are the
+    tokens in the cache, and pos and slot those of the step's tokens, all on the device: admit() and step() plan them."""
+
+    def __init__(self, blocks, heads, kv_heads, dim, batch, width: int, rope: moe.Rope, alpha=0.5):
+        table = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
+        super().__init__(blocks, heads, kv_heads, dim, batch, table, alpha)
+        cache = blocks[0].cache
+        self.rope, self.page, self.n_pages = rope, cache.page_size, cache.n_pages
+        self.lens.zero_()
+        self.free = torch.arange(self.n_pages, dtype=torch.int32, device="cuda")
+        self.n_free = torch.full((1,), self.n_pages, dtype=torch.int32, device="cuda")
+        self.slot, self.seq = torch.empty_like(self.pos), torch.empty_like(self.pos)
+        self.starts = torch.empty(batch + 1, dtype=torch.int32, device="cuda")
+        self.plan_ws = moe.pages_workspace(batch)
+
+    def admit(self, new_tokens: torch.Tensor, max_tokens: int) -> moe.PagePlan:
+        """Places for new_tokens[b] tokens of each sequence (the prompts')."""
+        return moe.page_plan(self.lens, new_tokens, self.page_table, self.free, self.n_free, self.page, self.n_pages,
+                             max_tokens, self.plan_ws)
+
+    def release(self, ended: torch.Tensor):
+        moe.page_release(self.lens, ended, self.page_table, self.free, self.n_free, self.page, self.plan_ws)
+
+    def place(self, b, q, k, v):
+        if b.window == 0:  # the layers of the whole context know no positions
+            return super().place(b, q, k, v)
+        return moe.rope_kv_write(q, k, v, b.cache, self.rope, self.pos, self.slot, self.attn_ws, q_out=q)
+
+    def step(self):
+        moe.page_plan(self.lens, None, self.page_table, self.free, self.n_free, self.page, self.n_pages, self.pos.shape[0],
+                      self.plan_ws, starts=self.starts, seq=self.seq, pos=self.pos, slot=self.slot)
+        return super().step()
+
+    def advance(self):
+        pass  # the plan has
 
 
 def build(n_layers: int, batch: int, context: int, heads=16, kv_heads=4, dim=128, d=2048, ffn=640, experts=384, page=64,
-          cache_dtype=MOE_E4M3, seed=1) -> Decoder:
+          cache_dtype=MOE_E4M3, seed=1, serve=False) -> Decoder:
     from gen import moegen
     g = torch.Generator(device="cuda").manual_seed(seed)
     width = -(-context // page)
@@ -97,6 +147,8 @@ def build(n_layers: int, batch: int, context: int, heads=16, kv_heads=4, dim=128
     layer = moe.Layer.from_host(moegen.make_layer(seed, d, ffn, experts, fp8=True, bias_var=0.5))
     blocks = [Block(layer if i == 0 else layer.clone(), heads, kv_heads, dim, n_pages, page,
                     0 if (i + 1) % FULL_EVERY == 0 else WINDOW, cache_dtype, g) for i in range(n_layers)]
+    if serve:
+        return Server(blocks, heads, kv_heads, dim, batch, width, moe.Rope(dim))
     return Decoder(blocks, heads, kv_heads, dim, batch, table)
 
 
@@ -109,7 +161,8 @@ def arguments(argv=None):
     ap.add_argument("--context", type=int, default=4096)
     ap.add_argument("--layers", type=int, default=5)
     ap.add_argument("--steps", type=int, default=50)
-    ap.add_argument("--cache", choices=("bf16", "e4m3"), default="e4m3")
+    ap.add_argument("--cache", choices=("bf16", "e4m3", "int4"), default="e4m3")
+    ap.add_argument("--serve", action="store_true")
     args = ap.parse_args(argv)
     for name in ("batch", "layers", "steps"):
         if getattr(args, name) < 1:
@@ -119,22 +172,37 @@ def arguments(argv=None):
     return args
 
 
+def fill(dec: Decoder, context: int, start: int):
+    """A context as if it had been decoded: random keys and values of every position."""
+    h, hk, batch = dec.heads, dec.kv_heads, dec.residual.shape[0]
+    serving = isinstance(dec, Server)
+    if serving:
+        plan = dec.admit(torch.full_like(dec.pos, start), batch * start)
+    for b in dec.blocks:
+        g = torch.Generator(device="cuda").manual_seed(7)
+        pos = torch.arange(start if serving else context, dtype=torch.int32, device="cuda")
+        for s in range(batch):
+            x = torch.randn(len(pos), h + 2 * hk, dec.dim, generator=g, device="cuda").bfloat16()
+            q, k, v = x[:, :h], x[:, h:h + hk], x[:, h + hk:]
+            if serving and b.window:
+                part = slice(s * start, (s + 1) * start)
+                moe.rope_kv_write(q, k, v, b.cache, dec.rope, plan.pos[part], plan.slot[part], dec.attn_ws, q_out=q)
+            else:
+                moe.kv_write(k, v, b.cache, pos, dec.page_table, dec.attn_ws, seq=torch.full_like(pos, s))
+
+
 def main():
     args = arguments()
-    dec = build(args.layers, args.batch, args.context, cache_dtype=MOE_E4M3 if args.cache == "e4m3" else MOE_BF16)
-    for b in dec.blocks:  # a context as if it had been decoded: random keys and values of every position
-        g = torch.Generator(device="cuda").manual_seed(7)
-        pos = torch.arange(args.context, dtype=torch.int32, device="cuda")
-        for s in range(args.batch):
-            kv = torch.randn(args.context, 2 * dec.kv_heads, dec.dim, generator=g, device="cuda").bfloat16()
-            moe.kv_write(kv[:, :dec.kv_heads], kv[:, dec.kv_heads:], b.cache, pos, dec.page_table, dec.attn_ws,
-                         seq=torch.full_like(pos, s))
+    dec = build(args.layers, args.batch, args.context, serve=args.serve,
+                cache_dtype={"bf16": MOE_BF16, "e4m3": MOE_E4M3, "int4": MOE_INT4}[args.cache])
     start = args.context - args.steps - SPARE
+    fill(dec, args.context, start)
     embed = torch.randn_like(dec.residual)
 
     def rewind():
-        dec.pos.fill_(start)
-        dec.lens.fill_(start + 1)
+        if not args.serve:  # (a server's steps go on: their pages are handed out)
+            dec.pos.fill_(start)
+            dec.lens.fill_(start + 1)
 
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -157,10 +225,10 @@ def main():
     end.record()
     torch.cuda.synchronize()
     us = begin.elapsed_time(end) * 1e3 / args.steps
-    for ws in (dec.attn_ws, dec.moe_ws):
+    for ws in (dec.attn_ws, dec.moe_ws) + ((dec.plan_ws,) if args.serve else ()):
         if moe.get_status(ws) != 0:
             raise SystemExit("a device-side error was recorded")
-    print(f"{args.layers} layers, batch {args.batch}, context {args.context}, {args.cache} cache: "
+    print(f"{args.layers} layers, batch {args.batch}, context {args.context}, {args.cache} cache{', serving' * args.serve}: "
           f"{us:.1f} us a step, {args.batch * 1e6 / us:.0f} tokens/s")
 
 

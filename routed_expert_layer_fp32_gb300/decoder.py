@@ -251,7 +251,8 @@ def pages_workspace(B: int, device="cuda") -> torch.Tensor:
 
 
 def _ints(name: str, t: torch.Tensor, n: int, dev: int) -> int:
-    if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+    # (numel and dim are a third of what the shape costs)
+    if t.dtype is not torch.int32 or t.numel() != n or t.dim() != 1 or t.get_device() != dev or not t.is_contiguous():
         raise _misfit(name, t, f"int32 [{n}], contiguous")
     return t.data_ptr()
 
