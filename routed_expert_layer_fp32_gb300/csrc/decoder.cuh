@@ -154,6 +154,8 @@ struct AttnArgs {
 
 size_t attn_workspace_bytes(const CacheDev& c, int n_heads, int B);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
+size_t attn_int4_workspace_bytes(const CacheDev& c, int n_heads);  // of these two, the part for INT4 caches
+cudaError_t launch_attn_int4(const AttnArgs& a, cudaStream_t s);
 
 // Calls f with a constant: the lanes of a row (a power of two that covers it with eight elements each), the cache's
 // kind of rows, or a value of the source's type.
