@@ -30,8 +30,8 @@ moe_status check_cache(const moe_kv_cache* c) {
   return MOE_OK;
 }
 
-CacheDev to_dev(const moe_kv_cache* c) {
-  CacheDev d;
+CacheScaled to_dev(const moe_kv_cache* c) {
+  CacheScaled d;
   d.n_pages = c->n_pages;
   d.page = c->page_size;
   d.heads = c->n_kv_heads;
@@ -179,8 +179,10 @@ moe_status moe_attn_decode(const moe_kv_cache* cache, const void* q, int64_t q_s
       (room / 32 + 1) * B * cache->n_kv_heads >= (int64_t(1) << 31) / ((group + 3) / 4))
     return MOE_ERR_UNSUPPORTED;
   if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
-  AttnArgs a;
-  a.cache = to_dev(cache);
+  AttnScaledArgs a;
+  a.cache = to_dev(cache);  // (without its scales)
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
   if (ws_bytes < attn_workspace_bytes(a.cache, n_heads, B)) return MOE_ERR_WORKSPACE;
   a.table = PageTable{page_table, B, max_pages, static_cast<int*>(ws)};
   a.q = static_cast<const __nv_bfloat16*>(q);

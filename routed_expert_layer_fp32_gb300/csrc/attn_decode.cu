@@ -32,7 +32,7 @@ size_t attn_workspace_bytes(const CacheDev& c, int n_heads, int) {
          });
 }
 
-cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_attn_decode(const AttnScaledArgs& a, cudaStream_t s) {
   if (a.cache.rows == RowKind::kInt4) return launch_attn_int4(a, s);
   return with_shape(a.cache, a.n_heads / a.cache.heads, [&](auto shape) { return launch<decltype(shape)>(a, s); });
 }

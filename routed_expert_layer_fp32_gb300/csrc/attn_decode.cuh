@@ -87,6 +87,7 @@ template <RowKind kRows_, int kDim_, int kHeads_, bool kShort = false>
 struct Shape {
   static constexpr RowKind kRows = kRows_;
   static constexpr bool kE4M3 = kRows == RowKind::kE4M3, kInt4 = kRows == RowKind::kInt4;
+  using Args = std::conditional_t<kInt4, AttnScaledArgs, AttnArgs>;
   static constexpr int kDim = kDim_;      // head_dim rounded up to 64, 128 or 256 (copies fill with zeros)
   static constexpr int kHeads = kHeads_;  // query heads of a segment
   static constexpr int kRow = kE4M3 ? kDim : kInt4 ? kDim / 2 : kDim * 2;  // bytes
@@ -1146,7 +1147,7 @@ __device__ __forceinline__ void for_constants(std::integer_sequence<int, I...>, 
 
 template <typename S>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attn_decode(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+    k_attn_decode(const typename S::Args a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                   int box, int copies, int page_boxes, uint32_t page_magic, int group, int head_blocks) {
   using Control = typename S::Control;
   using Compute = std::conditional_t<S::kE4M3, WarpE4M3<S>, WarpBf16<S>>;
@@ -1318,7 +1319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const int at = (lane + i * 32) * 16;
               if (at < S::kTokens * pitch && (copied >> scale_box[i] & 1))
                 cp_async16(to + 2 * S::kTokens + me * S::kScales + at,
-                           (me ? c.v_scale : c.k_scale) + int64_t(y) * pitch + (at - scale_box[i] * box * pitch));
+                           (me ? a.v_scale : a.k_scale) + int64_t(y) * pitch + (at - scale_box[i] * box * pitch));
             }
             const int r = lane * 16 & (S::kTokens - 1), i = r >> row_shift;
             const int y = __shfl_sync(0xffffffffu, row, i) + (r & (box - 1));
@@ -1573,7 +1574,7 @@ bool cache_map(CUtensorMap* map, const void* base, const CacheDev& c, int box, i
 }
 
 template <typename S>
-cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch(const typename S::Args& a, cudaStream_t s) {
   const CacheDev& c = a.cache;
   static std::atomic<int> ready[kMaxDevices];
   cudaError_t attr = cudaSuccess;

@@ -29,7 +29,7 @@ size_t attn_int4_workspace_bytes(const CacheDev& c, int n_heads) {
          });
 }
 
-cudaError_t launch_attn_int4(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_attn_int4(const AttnScaledArgs& a, cudaStream_t s) {
   const int room = a.table.max_pages * a.cache.page, longest = a.window > 0 ? std::min(a.window, room) : room;
   return with_shape(a.cache, a.n_heads / a.cache.heads, longest,
                     [&](auto shape) { return launch<decltype(shape)>(a, s); });

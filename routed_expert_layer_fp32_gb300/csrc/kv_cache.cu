@@ -31,7 +31,7 @@ __device__ __forceinline__ int64_t cache_row(const CacheDev& c, const PageTable&
 }
 
 template <int kLanes, RowKind kRows, typename Src>
-__global__ void __launch_bounds__(256) k_kv_write(CacheDev c, PageTable pt, const Src* __restrict__ k,
+__global__ void __launch_bounds__(256) k_kv_write(CacheOf<kRows> c, PageTable pt, const Src* __restrict__ k,
                                                   const Src* __restrict__ v, int64_t k_stride, int64_t v_stride, int T,
                                                   const int32_t* __restrict__ seq, const int32_t* __restrict__ pos) {
   const int t = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
@@ -52,14 +52,17 @@ __global__ void __launch_bounds__(256) k_kv_write(CacheDev c, PageTable pt, cons
 #pragma unroll
   for (int j = 0; j < kHeadsEach; ++j) {
     const int64_t row = row0 + int64_t(h0 + j) * c.page;
-    const bool write = row0 >= 0 && j < heads;
-    store_row<kLanes, kRows>(c, c.k, c.k_exp, c.k_scale, row, write, lane, kx[j]);
-    store_row<kLanes, kRows>(c, c.v, c.v_exp, c.v_scale, row, write, lane, vx[j]);
+    RowCode<kRows> kc, vc;
+    kc.template find<kLanes>(kx[j]);
+    vc.template find<kLanes>(vx[j]);
+    if (row0 < 0 || j >= heads) continue;
+    kc.store(c, c.k, c.k_exp, scales_of<kRows>(c, true), row, lane, 0, kx[j]);
+    vc.store(c, c.v, c.v_exp, scales_of<kRows>(c, false), row, lane, 1, vx[j]);
   }
 }
 
 template <int kLanes, RowKind kRows, typename Dst>
-__global__ void __launch_bounds__(256) k_kv_read(CacheDev c, PageTable pt, int T, const int32_t* __restrict__ seq,
+__global__ void __launch_bounds__(256) k_kv_read(CacheOf<kRows> c, PageTable pt, int T, const int32_t* __restrict__ seq,
                                                  const int32_t* __restrict__ pos, Dst* __restrict__ k_out,
                                                  Dst* __restrict__ v_out) {
   const int t = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
@@ -72,8 +75,8 @@ __global__ void __launch_bounds__(256) k_kv_read(CacheDev c, PageTable pt, int T
   for (int j = 0; j < kHeadsEach; ++j) {
     const int64_t row = row0 + int64_t(h0 + j) * c.page;
     const bool read = row0 >= 0 && j < heads;
-    k[j].load(c, c.k, c.k_exp, c.k_scale, row, read, lane);
-    v[j].load(c, c.v, c.v_exp, c.v_scale, row, read, lane);
+    k[j].load(c, c.k, c.k_exp, scales_of<kRows>(c, true), row, read, lane);
+    v[j].load(c, c.v, c.v_exp, scales_of<kRows>(c, false), row, read, lane);
   }
 #pragma unroll
   for (int j = 0; j < kHeadsEach; ++j) {
@@ -90,7 +93,7 @@ dim3 token_grid(int T, int lanes, int heads) {
 
 }  // namespace
 
-cudaError_t launch_kv_write(const CacheDev& c, const PageTable& pt, const void* k, const void* v, bool bf16,
+cudaError_t launch_kv_write(const CacheScaled& c, const PageTable& pt, const void* k, const void* v, bool bf16,
                             int64_t k_stride, int64_t v_stride, int T, const int32_t* seq, const int32_t* pos,
                             cudaStream_t s) {
   return with_lanes(c.dim, [&](auto lanes) {
@@ -98,22 +101,22 @@ cudaError_t launch_kv_write(const CacheDev& c, const PageTable& pt, const void* 
     return with_rows(c.rows, [&](auto rows) {
       return with_source(bf16, [&](auto src) {
         using Src = decltype(src);
-        return launch_pdl(k_kv_write<L, decltype(rows)::value, Src>, token_grid(T, L, c.heads), dim3(256), 0, s, c, pt,
-                          static_cast<const Src*>(k), static_cast<const Src*>(v), k_stride, v_stride, T, seq, pos);
+        return launch_pdl(k_kv_write<L, decltype(rows)::value, Src>, token_grid(T, L, c.heads), dim3(256), 0, s,
+                          CacheOf<decltype(rows)::value>(c), pt, static_cast<const Src*>(k), static_cast<const Src*>(v), k_stride, v_stride, T, seq, pos);
       });
     });
   });
 }
 
-cudaError_t launch_kv_read(const CacheDev& c, const PageTable& pt, int T, const int32_t* seq, const int32_t* pos,
+cudaError_t launch_kv_read(const CacheScaled& c, const PageTable& pt, int T, const int32_t* seq, const int32_t* pos,
                            void* k_out, void* v_out, bool bf16, cudaStream_t s) {
   return with_lanes(c.dim, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
     return with_rows(c.rows, [&](auto rows) {
       return with_source(bf16, [&](auto dst) {
         using Dst = decltype(dst);
-        return launch_pdl(k_kv_read<L, decltype(rows)::value, Dst>, token_grid(T, L, c.heads), dim3(256), 0, s, c, pt, T,
-                          seq, pos, static_cast<Dst*>(k_out), static_cast<Dst*>(v_out));
+        return launch_pdl(k_kv_read<L, decltype(rows)::value, Dst>, token_grid(T, L, c.heads), dim3(256), 0, s,
+                          CacheOf<decltype(rows)::value>(c), pt, T, seq, pos, static_cast<Dst*>(k_out), static_cast<Dst*>(v_out));
       });
     });
   });

@@ -101,47 +101,63 @@ __device__ __forceinline__ uint32_t int4_unit(uint32_t scale, uint32_t exp) {
   return (scale * 16u + (exp - kInt4Zero) * 128u) * 0x00010001u;
 }
 
-// Writes one row, if `write` holds (the same for the lanes of a group; all lanes of the warp come here).  x: the
-// lane's eight elements, zeros past the row's end.
-template <int kLanes, RowKind kRows>
-__device__ __forceinline__ void store_row(const CacheDev& c, uint8_t* pool, uint8_t* exps, uint8_t* scales, int64_t row,
-                                          bool write, int lane, float (&x)[8]) {
-  const bool mine = lane * 8 < c.dim;
-  if constexpr (kRows == RowKind::kBf16) {
-    if (write && mine) store_vec8(reinterpret_cast<__nv_bfloat16*>(pool) + row * c.dim + lane * 8, x);
-  } else if constexpr (kRows == RowKind::kE4M3) {
-    const uint32_t e = row_exponent(group_max8<kLanes>(x));
-    if (!write) return;
-    if (mine) *reinterpret_cast<uint2*>(pool + row * c.dim + lane * 8) = codes8(x, inverse_exp_value(e));
-    if (lane == 0) exps[row] = uint8_t(e);
-  } else {
-    float top = 0.0f;
+// How a row is held: found by all lanes of its group together, then written by them.  x: the lane's eight elements, zeros
+// past the row's end.
+template <RowKind kRows>
+struct RowCode {
+  uint32_t exp, scale;  // of the row, and (INT4) of the lane's sixteen elements
+  template <int kLanes>
+  __device__ __forceinline__ void find(const float (&x)[8]) {
+    if constexpr (kRows == RowKind::kE4M3) exp = row_exponent(group_max8<kLanes>(x));
+    if constexpr (kRows == RowKind::kInt4) {
+      float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max_or_nan(top, fabsf(x[i]));
-    top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    float row_top = top;
+      for (int i = 0; i < 8; ++i) top = max_or_nan(top, fabsf(x[i]));
+      top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      float row_top = top;
 #pragma unroll
-    for (int o = kLanes / 2; o > 1; o >>= 1) row_top = max_or_nan(row_top, __shfl_xor_sync(0xffffffffu, row_top, o));
-    if (!write) return;
-    const bool lost = !(row_top < INFINITY);
-    const uint32_t e = lost ? uint32_t(kInt4ExpNaN) : int4_row_exponent(row_top);
-    const uint32_t b = lost ? 127u : int4_scale_byte(top * __uint_as_float((254u - e) << 23));  // times 2^(127 - e)
-    if (mine) {
-      const float s = int4_scale(b) * __uint_as_float(e << 23);
-      // of the eight mantissas a scale has, each rounded to nearest, times powers of two
-      const float reciprocal =
-          kReciprocals[b & 7] * (__uint_as_float((139u - (b >> 3)) << 23) * __uint_as_float((254u - e) << 23));
-      if (__builtin_expect(e == kInt4ExpHigh, 0)) {  // magnitudes past 7 s
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -kInt4Most * s), kInt4Most * s);
-      }
-      reinterpret_cast<uint32_t*>(pool + row * (c.dim / 2))[lane] = int4_codes(x, s, reciprocal);
+      for (int o = kLanes / 2; o > 1; o >>= 1) row_top = max_or_nan(row_top, __shfl_xor_sync(0xffffffffu, row_top, o));
+      const bool lost = !(row_top < INFINITY);
+      exp = lost ? uint32_t(kInt4ExpNaN) : int4_row_exponent(row_top);
+      scale = lost ? 127u : int4_scale_byte(top * __uint_as_float((254u - exp) << 23));  // times 2^(127 - exp)
     }
-    // a byte of two lanes; those past the row's end fill its last word with zeros
-    const int pitch = scale_pitch(c.dim), at = lane >> 1;
-    if ((lane & 1) == 0 && at < pitch) scales[row * pitch + at] = uint8_t(mine ? b : 0u);
-    if (lane == 0) exps[row] = uint8_t(e);
   }
+  // exp_lane: who writes the exponent
+  __device__ __forceinline__ void store(const CacheOf<kRows>& c, uint8_t* pool, uint8_t* exps, uint8_t* scales, int64_t row,
+                                        int lane, int exp_lane, float (&x)[8]) const {
+    const bool mine = lane * 8 < c.dim;
+    if constexpr (kRows == RowKind::kBf16) {
+      if (mine) store_vec8(reinterpret_cast<__nv_bfloat16*>(pool) + row * c.dim + lane * 8, x);
+      return;
+    }
+    if constexpr (kRows == RowKind::kE4M3) {
+      if (mine) *reinterpret_cast<uint2*>(pool + row * c.dim + lane * 8) = codes8(x, inverse_exp_value(exp));
+    }
+    if constexpr (kRows == RowKind::kInt4) {
+      if (mine) {
+        const float s = int4_scale(scale) * __uint_as_float(exp << 23);
+        // of the eight mantissas a scale has, each rounded to nearest, times powers of two
+        const float reciprocal = kReciprocals[scale & 7] * (__uint_as_float((139u - (scale >> 3)) << 23) *
+                                                            __uint_as_float((254u - exp) << 23));
+        if (__builtin_expect(exp == kInt4ExpHigh, 0)) {  // magnitudes past 7 s
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -kInt4Most * s), kInt4Most * s);
+        }
+        reinterpret_cast<uint32_t*>(pool + row * (c.dim / 2))[lane] = int4_codes(x, s, reciprocal);
+      }
+      // a byte of two lanes; those past the row's end fill its last word with zeros
+      const int pitch = scale_pitch(c.dim), at = lane >> 1;
+      if ((lane & 1) == 0 && at < pitch) scales[row * pitch + at] = uint8_t(mine ? scale : 0u);
+    }
+    if (lane == exp_lane) exps[row] = uint8_t(exp);
+  }
+};
+
+// The scales of keys and values where there are any.
+template <RowKind kRows>
+__device__ __forceinline__ uint8_t* scales_of(const CacheOf<kRows>& c, bool keys) {
+  if constexpr (kRows == RowKind::kInt4) return keys ? c.k_scale : c.v_scale;
+  else return nullptr;
 }
 
 // One row's raw contents, loaded before they are needed (zeros for a row that is not there).
@@ -149,7 +165,7 @@ template <RowKind kRows>
 struct RawRow {
   uint4 w;
   uint32_t exp, scale;
-  __device__ __forceinline__ void load(const CacheDev& c, const uint8_t* pool, const uint8_t* exps, const uint8_t* scales,
+  __device__ __forceinline__ void load(const CacheOf<kRows>& c, const uint8_t* pool, const uint8_t* exps, const uint8_t* scales,
                                        int64_t row, bool there, int lane) {
     w = make_uint4(0u, 0u, 0u, 0u);
     exp = kRows == RowKind::kInt4 ? kInt4Zero : kExpBias;

@@ -238,9 +238,12 @@ __device__ __forceinline__ void place_rows(const RopeArgs& a, int t, int lane, i
     load(j + 1, next);
     const bool is_k = j < a.k.heads;
     if (is_k) h.turn(turn, with);
-    store_row<kLanes, kRows>(a.cache, is_k ? a.cache.k : a.cache.v, is_k ? a.cache.k_exp : a.cache.v_exp,
-                             is_k ? a.cache.k_scale : a.cache.v_scale,
-                             row0 + int64_t(is_k ? j : j - a.k.heads) * a.cache.page, row0 >= 0, lane, h.x);
+    RowCode<kRows> code;
+    code.template find<kLanes>(h.x);
+    if (row0 >= 0)
+      code.store(a.cache, is_k ? a.cache.k : a.cache.v, is_k ? a.cache.k_exp : a.cache.v_exp,
+                 is_k ? a.cache.k_scale : a.cache.v_scale, row0 + int64_t(is_k ? j : j - a.k.heads) * a.cache.page, lane, 0,
+                 h.x);
   }
 }
 
