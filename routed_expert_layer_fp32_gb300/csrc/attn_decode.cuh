@@ -56,6 +56,16 @@
 // padded to; a tcgen05 product has at least 64 rows on M, and its scores would have to travel
 // through TMEM.  Keys and values reach the registers by ldmatrix from the swizzled tiles, the
 // values transposed.
+//
+// An INT4 cache is read as a bf16 cache of its values, which bf16 holds exactly: the computing warps make the products'
+// operands of the codes, scales and exponents (Int4Operands).  There the bytes are 0.57 an element and no longer the
+// bound: 64 sequences of up to 16k tokens, 4 kv heads of 8 query heads, take 89 us, 59 % of the copy rate (bf16 200).
+// Without the products the copies take 61 us (a tile's copies are small: codes by TMA, scales and exponents by cp.async);
+// without the copies the products take 86, 45 of them to take codes apart.  That is 11 instructions for eight codes, of
+// pipes that take one every two cycles (AND-OR, shift, byte permutation and packed multiply-add alike; a measured 1.6
+// cycles each where two of them run side by side), so more warps do not help (twelve in place of eight, with fewer
+// registers each: 119 us against 110 at the time), nor does shifting by multiplication (IMAD.HI, four cycles: 110
+// against 102).
 #pragma once
 
 #include "batches.cuh"
@@ -443,11 +453,7 @@ struct Bf16Operands {
 // An INT4 cache's operands: bf16 numbers made of the codes, n s 2^e exactly, so that all that follows is as over a bf16
 // cache of these values.
 //
-// A code c = n + 8 of four bits at mantissa bits 3 to 6 of a bf16 number 128 makes it 128 + 8c = 192 + 8n: one AND and
-// OR for two codes, one in each half of a register, after a shift that the cache's order of bits makes unnecessary for
-// two of eight.  One fused multiply-add with (u, -192 u), u = s 2^e / 8, gives 8n u = n s 2^e without rounding.  u's bits
-// are the scale's byte, moved to where its three mantissa bits belong, plus the exponents (E + e - 15, all biased).  So
-// eight codes take 15 instructions, 11 of them to take the codes apart.
+// Codes are taken apart as kv_rows.cuh has it: eight take 11 instructions, and their u and -192 u three.
 //
 // Keys.  The products' element axis may be in any order that queries share: lane (g, t) reads a quarter t of rows g
 // and g + 8 in whole words, so that a word is two products' operands and a lane needs the scales of its own quarter only.

@@ -6,6 +6,9 @@
 // each.  So the place in the cache, three dependent loads away (sequence and position, then page, then
 // row), is looked up once for four rows, and four rows' loads are in flight together in every lane; a
 // row's largest magnitude is a few shuffles.
+//
+// Rows in 4 bits are bound by instructions more than by memory: writing takes about 23 a element (half of them the code
+// itself: kv_rows.cuh), reading 9.  16k tokens of 4 heads of 128: 14 us to write 43 MB, 11 to read them back.
 #include "kv_rows.cuh"
 
 namespace moe {
@@ -30,8 +33,10 @@ __device__ __forceinline__ int64_t cache_row(const CacheDev& c, const PageTable&
   return int64_t(page) * c.heads * c.page + (p - slot * c.page);
 }
 
+// INT4 is bound by what its warps issue, and is better with a few registers less and a fifth more of them (16k tokens
+// written and read back 26.5 -> 25.0 us; with a quarter of the registers less again 25.9).
 template <int kLanes, RowKind kRows, typename Src>
-__global__ void __launch_bounds__(256) k_kv_write(CacheOf<kRows> c, PageTable pt, const Src* __restrict__ k,
+__global__ void __launch_bounds__(256, kRows == RowKind::kInt4 ? 5 : 1) k_kv_write(CacheOf<kRows> c, PageTable pt, const Src* __restrict__ k,
                                                   const Src* __restrict__ v, int64_t k_stride, int64_t v_stride, int T,
                                                   const int32_t* __restrict__ seq, const int32_t* __restrict__ pos) {
   const int t = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
