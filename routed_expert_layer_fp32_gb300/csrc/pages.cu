@@ -13,7 +13,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 1024;  // at most, of the CTA with the sums
 constexpr int kShort = 4096;  // tokens or pages that the first CTA does itself
 
 // Exclusive sum over the CTA; `part` holds a value a warp.  `all` receives the total.
@@ -29,7 +29,7 @@ __device__ __forceinline__ T block_exclusive(T v, T* part, T& all) {
   __syncthreads();  // an earlier use of `part` is over
   if (lane == 31) part[warp] = upto;
   __syncthreads();
-  T w = lane < kThreads / 32 ? part[lane] : T(0);
+  T w = lane < int(blockDim.x >> 5) ? part[lane] : T(0);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const T x = __shfl_up_sync(0xffffffffu, w, o);
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) k_page_plan(PlanArgs a) {
   pdl_begin();
   int* status = reinterpret_cast<int*>(a.ws);
   if (threadIdx.x == 0) refused_any = given = 0;
-  const int per = (a.B + kThreads - 1) / kThreads;
+  const int threads = blockDim.x, per = (a.B + threads - 1) / threads;
   const int b0 = min(a.B, int(threadIdx.x) * per), b1 = min(a.B, b0 + per);
   const int n_free = free_count(a.n_free, a.n_pages, status);
   const int room = a.max_pages * a.page;
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) k_page_plan(PlanArgs a) {
   }
   if constexpr (kAll) {
     __syncthreads();  // starts, first and lens_out of all threads
-    for (int t = threadIdx.x; t < a.max_tokens; t += kThreads) {
+    for (int t = threadIdx.x; t < a.max_tokens; t += threads) {
       int b = -1, pos = -1, slot = -1;
       if (t < total) {
         b = sequence_of(a.starts, 0, a.B, t);
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) k_page_release(ReleaseArgs a) {
   __shared__ int64_t part[kThreads / 32];
   pdl_begin();
   int* status = reinterpret_cast<int*>(a.ws);
-  const int per = (a.B + kThreads - 1) / kThreads;
+  const int threads = blockDim.x, per = (a.B + threads - 1) / threads;
   const int b0 = min(a.B, int(threadIdx.x) * per), b1 = min(a.B, b0 + per);
   const int n_free = free_count(a.n_free, a.n_pages, status);
   const int room = a.max_pages * a.page;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads) k_page_release(ReleaseArgs a) {
   }
   if constexpr (kAll) {
     __syncthreads();
-    for (int b = threadIdx.x >> 5; b < a.B; b += kThreads / 32)
+    for (int b = threadIdx.x >> 5; b < a.B; b += threads / 32)
       give_back(a, b, places[b], places[b + 1] - places[b], threadIdx.x & 31, 32);
   }
 }
@@ -247,19 +247,25 @@ __global__ void __launch_bounds__(128) k_page_give_back(ReleaseArgs a) {
     give_back(a, b, places[b], places[b + 1] - places[b], threadIdx.x, 128);
 }
 
+// Whole warps for as many sequences or tokens, up to kThreads: a small CTA starts and meets sooner (a step of 64: 3.6 -> 3.2
+// us).
+int threads_for(int64_t n) { return int(std::min<int64_t>(kThreads, std::max<int64_t>(1, (n + 31) / 32) * 32)); }
+
 }  // namespace
 
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t s) {
-  if (a.max_tokens <= kShort) return launch_pdl(k_page_plan<true>, dim3(1), dim3(kThreads), 0, s, a);
-  const cudaError_t e = launch_pdl(k_page_plan<false>, dim3(1), dim3(kThreads), 0, s, a);
+  if (a.max_tokens <= kShort)
+    return launch_pdl(k_page_plan<true>, dim3(1), dim3(threads_for(std::max(a.B, a.max_tokens))), 0, s, a);
+  const cudaError_t e = launch_pdl(k_page_plan<false>, dim3(1), dim3(threads_for(a.B)), 0, s, a);
   if (e != cudaSuccess) return e;
   const int each = kTokenThreads * kTokensEach;
   return launch_pdl(k_page_tokens, dim3((a.max_tokens + each - 1) / each), dim3(kTokenThreads), 0, s, a);
 }
 
 cudaError_t launch_page_release(const ReleaseArgs& a, cudaStream_t s) {
-  if (int64_t(a.B) * a.max_pages <= kShort) return launch_pdl(k_page_release<true>, dim3(1), dim3(kThreads), 0, s, a);
-  const cudaError_t e = launch_pdl(k_page_release<false>, dim3(1), dim3(kThreads), 0, s, a);
+  if (int64_t(a.B) * a.max_pages <= kShort)
+    return launch_pdl(k_page_release<true>, dim3(1), dim3(threads_for(int64_t(a.B) * a.max_pages)), 0, s, a);
+  const cudaError_t e = launch_pdl(k_page_release<false>, dim3(1), dim3(threads_for(a.B)), 0, s, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_page_give_back, dim3(std::min(a.B, 2048)), dim3(128), 0, s, a);
 }

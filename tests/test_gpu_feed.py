@@ -225,6 +225,33 @@ def test_attention_ignores_what_it_does_not_see(moe, dim):
     assert attend(moe, gen(dim), lens, 4, 2, dim, page, window, mutate=rubbish) == 0
 
 
+@pytest.mark.parametrize("dim,page,hk", [(128, 4096, 1), (64, 1024, 3), (128, 16, 70), (256, 4096, 2)])
+def test_attention_of_large_pages_and_many_heads(moe, dim, page, hk):
+    assert attend(moe, gen(dim + page), [300, 1, 77], 2 * hk, hk, dim, page, width=1 if page > 300 else None) == 0
+
+
+def test_two_streams_with_a_workspace_each(moe):
+    """Calls on two streams at once, over one cache."""
+    g = gen(55)
+    pools, (k, v) = host_cache(g, 64, 2, 64, 128)
+    cache = moe.KVCache(*[t.cuda() for t in pools])
+    table = torch.randperm(64, generator=g).view(2, 32).int()
+    lens = [ints([2000, 1500]), ints([700, 2048])]
+    q = torch.randn(2, 2, 16, 128, generator=g).to(BF)
+    dev, t = q.cuda(), table.cuda()
+    ws = [moe.attn_workspace(cache, 16, 2) for _ in range(2)]
+    alone = [moe.attn_decode(dev[i], cache, lens[i], t, ws[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(moe.attn_decode(dev[i], cache, lens[i], t, ws[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert moe.get_status(ws[i]) == 0 and all(torch.equal(o_, alone[i]) for o_ in outs[i])
+
+
 def test_attention_with_bad_pages(moe):
     def bad(pools, table, lens_t):
         table[0, 1], table[1, 0], table[1, 2] = -1, 1 << 20, 9999
@@ -359,6 +386,53 @@ def test_plan(moe, B, page, top, more, spare):
     planned(moe, lens, new, table, free, n_free, page, sum(new) // 2)  # a list without room for all
 
 
+def test_plan_and_release_of_very_many(moe):
+    """65536 sequences and a list of 2^20 places, against the formulas in whole tensors (the oracle goes one by one)."""
+    B, page, most = 65536, 16, 1 << 20
+    g = gen(77)
+    lens, new = torch.randint(0, 200, (B,), generator=g), torch.randint(0, 33, (B,), generator=g)
+    held, wanted = (lens + page - 1) // page, (lens + new + page - 1) // page
+    ends = new.cumsum(0)
+    fits = ends <= most
+    got = torch.where(fits, wanted - held, torch.zeros_like(held))
+    n_pages = int(held.sum() + got.sum())
+    order = torch.randperm(n_pages, generator=g)
+    width = int(wanted.max())
+    table, first = torch.full((B, width), -1), held.cumsum(0) - held
+    column = torch.arange(width)
+    table = torch.where(column < held[:, None], order[(first[:, None] + column).clamp(max=n_pages - 1)], table)
+    free = torch.zeros(n_pages, dtype=torch.int64)
+    n_free = int(got.sum())
+    free[:n_free] = order[int(held.sum()):]
+    dev = [t.int().cuda() for t in (lens, new, table, free)]
+    nf, ws = ints([n_free]), moe.pages_workspace(B)
+    plan = moe.page_plan(*dev, nf, page, n_pages, most, ws)
+    assert moe.get_status(ws) == (0 if fits.all() else -9)
+    take = got.cumsum(0) - got
+    nth = column - held[:, None]
+    mine = (nth >= 0) & (nth < got[:, None])
+    table[mine] = free[(n_free - 1 - take[:, None] - nth)[mine]]
+    assert torch.equal(dev[2].cpu(), table.int()) and int(plan.n_free) == 0
+    after = lens + torch.where(fits, new, torch.zeros_like(new))
+    assert torch.equal(plan.lens.cpu(), after.int())
+    starts = torch.cat([torch.zeros(1, dtype=torch.int64), ends]).clamp(max=most)
+    assert torch.equal(plan.starts.cpu(), starts.int())
+    seq = torch.repeat_interleave(torch.arange(B), new)[:most]
+    pos = lens[seq] + torch.arange(len(seq)) - (ends - new)[seq]
+    ok = fits[seq]
+    slot = table[seq, (pos // page).clamp(max=width - 1)] * page + pos % page
+    pad = most - len(seq)
+    for mine, want in ((plan.seq, seq), (plan.pos, torch.where(ok, pos, -1)), (plan.slot, torch.where(ok, slot, -1))):
+        assert torch.equal(mine.cpu(), torch.cat([want, torch.full((pad,), -1)]).int())
+    ended = torch.randint(0, 2, (B,), generator=g).bool()
+    moe.page_release(dev[0], ended.cuda(), dev[2], dev[3], nf, page, ws)
+    assert moe.get_status(ws) == 0
+    back = torch.where(ended, (after + page - 1) // page, torch.zeros_like(after))
+    assert torch.equal(dev[0].cpu(), torch.where(ended, torch.zeros_like(after), after).int())
+    assert nf.tolist() == [int(back.sum())]
+    assert torch.equal(dev[3].cpu()[: int(back.sum())], table[column < back[:, None]].int())
+
+
 def test_plan_edges(moe):
     planned(moe, [0], [0], [[-1]], [3, 1, 0, 2], 4, 16, 5)
     planned(moe, [16, 0, 5], None, [[0, -1], [-1, -1], [1, -1]], [2, 3, 0, 0], 2, 16, 8)
@@ -455,6 +529,9 @@ def test_rope(moe, dim, rot, interleaved, kind):
     want, tol = fo.turned(x[:, 1:1 + heads], pos, freq, magnitude, interleaved, out=kind)
     close(got, want, tol, "turned")
     assert torch.equal(got[..., rot:], part[..., rot:])
+    wide = torch.full((T, heads + 1, dim), 7.0, dtype=kind).cuda()
+    moe.rope(part, table, pos.cuda(), out=wide[:, :heads])  # rows that lie further apart
+    assert torch.equal(wide[:, :heads], got) and (wide[:, heads] == 7).all()
     back = moe.rope(part, table, pos.cuda(), inverse=True)
     want, tol = fo.turned(x[:, 1:1 + heads], pos, freq, magnitude, interleaved, inverse=True, out=kind)
     close(back, want, tol, "turned back")
@@ -472,6 +549,17 @@ def test_rope_scalings_and_sizes(moe, scaling, T, heads):
     x, pos = torch.randn(T, heads, 64, generator=g), torch.randint(0, 40000, (T,), generator=g).int()
     want, tol = fo.turned(x, pos, freq, magnitude, False)
     close(moe.rope(x.cuda(), table, pos.cuda()), want, tol, "turned")
+
+
+@pytest.mark.parametrize("kind", [BF, F32])
+def test_rope_of_very_many_heads_and_tokens(moe, kind):
+    table = moe.Rope(8)
+    freq, m = fo.frequencies(8)
+    for T, heads in ((3, 1024), (70001, 1)):
+        g = gen(T)
+        x, pos = torch.randn(T, heads, 16, generator=g).to(kind), torch.randint(0, 9000, (T,), generator=g).int()
+        want, tol = fo.turned(x, pos, freq, m, False, out=kind)
+        close(moe.rope(x.cuda(), table, pos.cuda()), want, tol, "turned")
 
 
 def test_rope_of_given_frequencies_and_no_tokens(moe):
@@ -547,6 +635,9 @@ def test_rope_kv_write(moe, kind, src, dim, rot, interleaved, T, heads, hk):
     moe.kv_write(turned, v.float().contiguous(), other, where.cuda(), ints([[0, 1, 2, 3]]), ws, seq=ints([0] * T))
     for a, b in zip(pools, [t for t in (other.k, other.v, other.k_exp, other.v_exp, other.k_scale, other.v_scale) if t is not None]):
         assert torch.equal(a, b)
+    apart = torch.full((T, heads + 1, dim), 7.0, dtype=BF).cuda()
+    moe.rope_kv_write(q, k, v, cache, table, pos.cuda(), slot.cuda(), ws, q_out=apart[:, 1:])
+    assert torch.equal(apart[:, 1:], got) and (apart[:, 0] == 7).all()
     if src is BF:  # queries in place
         assert moe.rope_kv_write(q, k, v, cache, table, pos.cuda(), slot.cuda(), ws, q_out=q) is q
         assert torch.equal(q, got)
