@@ -61,11 +61,11 @@
 // operands of the codes, scales and exponents (Int4Operands).  There the bytes are 0.57 an element and no longer the
 // bound: 64 sequences of up to 16k tokens, 4 kv heads of 8 query heads, take 89 us, 59 % of the copy rate (bf16 200).
 // Without the products the copies take 61 us (a tile's copies are small: codes by TMA, scales and exponents by cp.async);
-// without the copies the products take 86, 45 of them to take codes apart.  That is 11 instructions for eight codes, of
-// pipes that take one every two cycles (AND-OR, shift, byte permutation and packed multiply-add alike; a measured 1.6
-// cycles each where two of them run side by side), so more warps do not help (twelve in place of eight, with fewer
-// registers each: 119 us against 110 at the time), nor does shifting by multiplication (IMAD.HI, four cycles: 110
-// against 102).
+// without the copies the products take 86, 45 of them to take codes apart.  That is 11 instructions for eight codes, and
+// an AND-OR, a shift, a byte permutation and a packed multiply-add take two cycles each of a scheduler, the last not beside
+// the others (ANDs and packed multiply-adds in turn: 2.1 cycles each with two warps, 1.8 with four; ANDs and integer
+// multiply-adds 1.1).  So more warps do not help (twelve in place of eight, with fewer registers each: 119 us against 110
+// at the time), nor does shifting by multiplication (the high half takes four cycles: 110 against 102).
 #pragma once
 
 #include "batches.cuh"
