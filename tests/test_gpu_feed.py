@@ -199,6 +199,32 @@ def test_attention_lengths(moe, n):
     assert attend(moe, gen(n), [n], 2, 2, 96, 16, window=n - 1) == 0
 
 
+# A page table wide enough for segments of more than 1024 tokens takes the kernels with larger tiles.
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 192])
+@pytest.mark.parametrize("H,hk", [(1, 1), (8, 1), (6, 2), (12, 1), (32, 2)])
+def test_attention_shapes_with_large_tiles(moe, dim, H, hk):
+    assert attend(moe, gen(dim * 10 + H), [1, 0, 130, 33, 257, 300], H, hk, dim, 64, width=17) == 0
+
+
+@pytest.mark.parametrize("page", [16, 48, 64, 240, 256])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window", [0, 1025])
+def test_attention_pages_and_windows_with_large_tiles(moe, page, dim, window):
+    assert attend(moe, gen(page + dim), [1, 300, 1100, 255, 0, 256, 1300], 10, 1, dim, page, window,
+                  width=-(-1301 // page)) == 0
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 255, 256, 257, 511, 512, 513])
+def test_attention_lengths_with_large_tiles(moe, n):
+    assert attend(moe, gen(n), [n, 7], 7, 1, 128, 64, width=17) == 0
+    assert attend(moe, gen(n), [n, 7], 2, 2, 64, 16, width=65) == 0
+
+
+def test_attention_of_many_short_sequences_with_large_tiles(moe):
+    rng = random.Random(14)
+    assert attend(moe, gen(15), [rng.randint(0, 90) for _ in range(150)], 8, 2, 64, 256, width=5) == 0
+
+
 def test_attention_of_many_sequences(moe):
     rng = random.Random(4)
     assert attend(moe, gen(11), [rng.randint(0, 90) for _ in range(331)], 8, 2, 64, 16) == 0
@@ -223,6 +249,8 @@ def test_attention_ignores_what_it_does_not_see(moe, dim):
             t.copy_(torch.where(keep, t, dirt))
 
     assert attend(moe, gen(dim), lens, 4, 2, dim, page, window, mutate=rubbish) == 0
+    window = 1030  # with large tiles: everything but what lies behind the last token is seen
+    assert attend(moe, gen(dim), lens, 4, 2, dim, page, window, mutate=rubbish, width=65) == 0
 
 
 @pytest.mark.parametrize("dim,page,hk", [(128, 4096, 1), (64, 1024, 3), (128, 16, 70), (256, 4096, 2)])
@@ -258,6 +286,7 @@ def test_attention_with_bad_pages(moe):
         table[2] = -7
 
     assert attend(moe, gen(3), [60, 60, 40], 4, 2, 128, 16, mutate=bad) == -8
+    assert attend(moe, gen(3), [60, 60, 40], 4, 2, 128, 16, mutate=bad, width=65) == -8
 
     def long(pools, table, lens_t):
         lens_t[0] = 1000
