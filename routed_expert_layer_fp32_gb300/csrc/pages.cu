@@ -3,7 +3,9 @@
 // Both are prefix sums over the sequences (tokens, then the pages of those whose tokens fit) followed by a pass over
 // what they address (the new tokens, or the pages given back).  The sums are one CTA's work, a run of sequences a
 // thread; the pass is the same CTA's where it is short, as in a decode step, else a second kernel's, a thread four
-// tokens or a CTA a sequence.  What bounds the small calls is the chain lengths -> sums -> table -> places.
+// tokens or a CTA a sequence.  What bounds the calls is the chain lengths -> sums -> table -> places: a step of 64
+// sequences 3.3 us, 192 prompts with 342 thousand places 7.1 (4.9 MB: 0.7 at the copy rate), 64 of 256 sequences given
+// back 4.7.  (Keeping the starts in shared memory for the search of a place's sequence changed nothing.)
 //
 // In place: the sums are done, and everything that comes from the lengths and n_free is written down, before either
 // is overwritten.  A new page's entry is written by the thread of its first token, and the stack itself is not written by a

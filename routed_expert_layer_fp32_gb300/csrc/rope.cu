@@ -14,6 +14,10 @@
 // eight elements in a row (their scales and codes), so for keys and values a lane has those, and loads its keys' partners
 // as well (they are in L1: another lane of the group loads them).  The heads of a token are shared out over blocks: those
 // of the queries, then those of keys and values.
+//
+// Measured: 16k tokens of 32 heads of 128 bf16 turned 41.4 us, 97 % of the copy rate (with a row's eight elements a lane
+// and partners loaded for the queries too, one head ahead, 74.7); with 4 kv heads into a bf16 cache 59.7 us, 84 % (two or
+// four rows ahead 59.7 and 70.7, for their registers; two heads of keys and values a block 62.4); one token 1.8 us.
 #include "kv_rows.cuh"
 
 namespace moe {
@@ -21,7 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One lane's cosines and sines: element i becomes x_i cs[i].x + partner_i cs[i].y.
+// One lane's cosines and sines: element i becomes x_i c[i] + partner_i s[i].
 struct Turn {
   float c[8], s[8];
 };
