@@ -41,8 +41,9 @@ CacheScaled to_dev(const moe_kv_cache* c) {
   d.v = static_cast<uint8_t*>(c->v);
   d.k_exp = c->k_exp;
   d.v_exp = c->v_exp;
-  d.k_scale = c->k_scale;
-  d.v_scale = c->v_scale;
+  // a descriptor of a program built before INT4 caches ends with v_exp
+  d.k_scale = d.rows == RowKind::kInt4 ? c->k_scale : nullptr;
+  d.v_scale = d.rows == RowKind::kInt4 ? c->v_scale : nullptr;
   return d;
 }
 
@@ -180,9 +181,10 @@ moe_status moe_attn_decode(const moe_kv_cache* cache, const void* q, int64_t q_s
     return MOE_ERR_UNSUPPORTED;
   if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
   AttnScaledArgs a;
-  a.cache = to_dev(cache);  // (without its scales)
-  a.k_scale = cache->k_scale;
-  a.v_scale = cache->v_scale;
+  const CacheScaled c = to_dev(cache);
+  a.cache = c;  // (without its scales)
+  a.k_scale = c.k_scale;
+  a.v_scale = c.v_scale;
   if (ws_bytes < attn_workspace_bytes(a.cache, n_heads, B)) return MOE_ERR_WORKSPACE;
   a.table = PageTable{page_table, B, max_pages, static_cast<int*>(ws)};
   a.q = static_cast<const __nv_bfloat16*>(q);
