@@ -283,7 +283,7 @@ __device__ __forceinline__ Span span_of_len(const AttnArgs& a, int len) {
 
 template <typename S>
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
-  return span_of_len<S>(a, __ldg(a.lens + b));
+  return span_of_len<S>(a, a.lens[b]);
 }
 
 // Walks a CTA's part of the line, segment by segment.  The length of the sequence to come is read one
@@ -301,7 +301,7 @@ struct Walk {
     hi = hi_;
     b = b0;
     if (pos >= hi) return;
-    len_to_come = __ldg(a.lens + min(b + 1, a.B - 1));
+    len_to_come = a.lens[min(b + 1, a.B - 1)];
     span = span_of<S>(a, b);
     seg = unsigned(off0) / unsigned(span.tiles);
     tile = off0 - seg * span.tiles;
@@ -316,7 +316,7 @@ struct Walk {
       seg = 0;
       do {
         span = span_of_len<S>(a, len_to_come);
-        len_to_come = __ldg(a.lens + min(++b + 1, a.B - 1));
+        len_to_come = a.lens[min(++b + 1, a.B - 1)];
       } while (span.tiles == 0);  // pos < hi: a sequence with tiles follows
     }
     take = min(span.tiles, hi - pos);
@@ -423,7 +423,7 @@ struct Bf16Operands {
       for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll
         for (int i = 0; i < 2; ++i)  // head_dim is a multiple of 16
-          r[nb][ks][i] = nb * 8 + g < heads && ks * 16 < dim ? __ldg(row + ks * 8 + i * 4) : 0u;
+          r[nb][ks][i] = nb * 8 + g < heads && ks * 16 < dim ? row[ks * 8 + i * 4] : 0u;
     }
 #pragma unroll
     for (int nb = 0; nb < kNB; ++nb)
@@ -511,7 +511,7 @@ struct Int4Operands {
       for (int w = 0; w < kWords; ++w) {
         const int d = t * (S::kDim / 4) + w * 8;
         u[nb][w] = nb * 8 + g < heads && d < dim
-                       ? __ldg(reinterpret_cast<const uint4*>(q + int64_t(nb * 8 + g) * dim + d))
+                       ? *reinterpret_cast<const uint4*>(q + int64_t(nb * 8 + g) * dim + d)
                        : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
@@ -857,7 +857,7 @@ struct WarpE4M3 {
       float top = 0.0f;
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks)
-        u[ks] = h < heads && ks * 32 + odd * 16 < dim ? __ldg(row + ks * 8) : make_uint2(0u, 0u);
+        u[ks] = h < heads && ks * 32 + odd * 16 < dim ? row[ks * 8] : make_uint2(0u, 0u);
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[ks].x << 16)), fabsf(__uint_as_float(u[ks].x & 0xffff0000u))));
@@ -1215,7 +1215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     mine += span_of<S>(a, b).tiles * segs;
-    if (blockIdx.x == 0 && __ldg(a.lens + b) > a.table.max_pages * c.page) report_bad_page(a.table.status_flags);
+    if (blockIdx.x == 0 && a.lens[b] > a.table.max_pages * c.page) report_bad_page(a.table.status_flags);
   }
   int upto = mine;
 #pragma unroll
@@ -1273,7 +1273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int i = t_begin * boxes + rel + lane, p = i << row_shift;
           const int slot = page_boxes == 1 ? i : __umulhi(i, page_magic);  // i / page_boxes
           const bool wanted = rel + lane < walk.take * boxes && p < walk.span.end && p + box > walk.span.first;
-          return Boxes{wanted ? __ldg(pages + slot) : -1, (i - slot * page_boxes) << row_shift};
+          return Boxes{wanted ? pages[slot] : -1, (i - slot * page_boxes) << row_shift};
         };
         Boxes cur = look_up(0), ahead = look_up(32);
         for (int n = 0; n < walk.take; ++n, ++it) {

@@ -45,6 +45,10 @@ __host__ __device__ inline int row_bytes(RowKind rows, int dim) {
 }
 __host__ __device__ inline int scale_pitch(int dim) { return (dim + 63) / 64 * 4; }
 
+// What other operators' kernels write (places, lengths, pages, queries, rows) is read by plain loads, in all of these
+// files: the writer may still run when the reader's grid starts (pdl_begin), and a load through the read-only path (__ldg,
+// or a const __restrict__ pointer) is for data that nobody writes while the grid lives.
+
 // A page table on the device and where its violations are recorded.
 struct PageTable {
   const int32_t* pages;

@@ -20,12 +20,12 @@ constexpr int kHeadsEach = 2;
 // or refused token.  Head h's row is h * page further.
 __device__ __forceinline__ int64_t cache_row(const CacheDev& c, const PageTable& pt, const int32_t* seq,
                                              const int32_t* pos, int t) {
-  const int p = __ldg(pos + t);
-  const int s = seq ? __ldg(seq + t) : t;
+  const int p = pos[t];
+  const int s = seq ? seq[t] : t;
   if (p < 0) return -1;
   const int slot = unsigned(p) / unsigned(c.page);
   int page = -1;
-  if (s >= 0 && s < pt.n_seqs && slot < pt.max_pages) page = __ldg(pt.pages + int64_t(s) * pt.max_pages + slot);
+  if (s >= 0 && s < pt.n_seqs && slot < pt.max_pages) page = pt.pages[int64_t(s) * pt.max_pages + slot];
   if (page < 0 || page >= c.n_pages) {
     report_bad_page(pt.status_flags);
     return -1;
@@ -36,9 +36,9 @@ __device__ __forceinline__ int64_t cache_row(const CacheDev& c, const PageTable&
 // INT4 is bound by what its warps issue, and is better with a few registers less and a fifth more of them (16k tokens
 // written and read back 26.5 -> 25.0 us; with a quarter of the registers less again 25.9).
 template <int kLanes, RowKind kRows, typename Src>
-__global__ void __launch_bounds__(256, kRows == RowKind::kInt4 ? 5 : 1) k_kv_write(CacheOf<kRows> c, PageTable pt, const Src* __restrict__ k,
-                                                  const Src* __restrict__ v, int64_t k_stride, int64_t v_stride, int T,
-                                                  const int32_t* __restrict__ seq, const int32_t* __restrict__ pos) {
+__global__ void __launch_bounds__(256, kRows == RowKind::kInt4 ? 5 : 1) k_kv_write(CacheOf<kRows> c, PageTable pt, const Src* k,
+                                                  const Src* v, int64_t k_stride, int64_t v_stride, int T,
+                                                  const int32_t* seq, const int32_t* pos) {
   const int t = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const int h0 = blockIdx.y * kHeadsEach, heads = min(kHeadsEach, c.heads - h0);
   const bool mine = t < T && lane * 8 < c.dim;
@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(256, kRows == RowKind::kInt4 ? 5 : 1) k_kv_wri
 }
 
 template <int kLanes, RowKind kRows, typename Dst>
-__global__ void __launch_bounds__(256) k_kv_read(CacheOf<kRows> c, PageTable pt, int T, const int32_t* __restrict__ seq,
-                                                 const int32_t* __restrict__ pos, Dst* __restrict__ k_out,
+__global__ void __launch_bounds__(256) k_kv_read(CacheOf<kRows> c, PageTable pt, int T, const int32_t* seq,
+                                                 const int32_t* pos, Dst* __restrict__ k_out,
                                                  Dst* __restrict__ v_out) {
   const int t = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const int h0 = blockIdx.y * kHeadsEach, heads = min(kHeadsEach, c.heads - h0);

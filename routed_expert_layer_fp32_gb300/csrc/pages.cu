@@ -69,7 +69,7 @@ __device__ __forceinline__ void place_token(const PlanArgs& a, int t, int b, int
   if (nth < held) {
     page = a.table[int64_t(b) * a.max_pages + nth];
   } else {
-    page = __ldg(a.free_pages + (first - (nth - held)));
+    page = a.free_pages[first - (nth - held)];
     if (row == 0) a.table[int64_t(b) * a.max_pages + nth] = page;
   }
   if (page >= 0 && page < a.n_pages) slot = page * a.page + row;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) k_page_plan(PlanArgs a) {
   const int b0 = min(a.B, int(threadIdx.x) * per), b1 = min(a.B, b0 + per);
   const int n_free = free_count(a.n_free, a.n_pages, status);
   const int room = a.max_pages * a.page;
-  auto wanted = [&](int b) { return a.new_tokens ? max(__ldg(a.new_tokens + b), 0) : 1; };
+  auto wanted = [&](int b) { return a.new_tokens ? max(a.new_tokens[b], 0) : 1; };
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) mine += wanted(b);
   int64_t total;
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kTokenThreads) k_page_tokens(PlanArgs a) {
 __device__ __forceinline__ void give_back(const ReleaseArgs& a, int b, int at, int n, int lane, int lanes) {
   for (int j = lane; j < n; j += lanes) {
     const int64_t to = int64_t(at) + j;
-    if (to < a.n_pages) a.free_pages[to] = __ldg(a.table + int64_t(b) * a.max_pages + j);
+    if (to < a.n_pages) a.free_pages[to] = a.table[int64_t(b) * a.max_pages + j];
   }
 }
 

@@ -172,7 +172,7 @@ __device__ __forceinline__ void turn_queries(const RopeArgs& a, int t, int lane,
   };
   fetch(j0);
   float c[4], s[4];
-  const int pos = __ldg(a.pos + t);
+  const int pos = a.pos[t];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 cs = turned ? cos_sin(__ldg(r.turns + 4 * lane + i), pos, r.magnitude) : make_float2(1.0f, 0.0f);
@@ -221,7 +221,7 @@ __device__ __forceinline__ void place_rows(const RopeArgs& a, int t, int lane, i
   const Partners with(a.rope, e0);
   int64_t row0 = -1;  // of head 0
   if (here) {
-    const int slot = __ldg(a.slot + t), page = unsigned(slot) / unsigned(a.cache.page);
+    const int slot = a.slot[t], page = unsigned(slot) / unsigned(a.cache.page);
     if (slot >= 0) {
       if (page < a.cache.n_pages) row0 = int64_t(page) * a.cache.heads * a.cache.page + (slot - page * a.cache.page);
       else report_bad_page(a.status_flags);
@@ -236,7 +236,7 @@ __device__ __forceinline__ void place_rows(const RopeArgs& a, int t, int lane, i
   Head<Src> next;
   load(j0, next);
   Turn turn;
-  if (j0 < a.k.heads) turn_of(a.rope, here ? __ldg(a.pos + t) : 0, mine ? e0 : a.rope.dim, a.inverse, turn);
+  if (j0 < a.k.heads) turn_of(a.rope, here ? a.pos[t] : 0, mine ? e0 : a.rope.dim, a.inverse, turn);
   for (int j = j0; j < j1; ++j) {
     Head<Src> h = next;
     load(j + 1, next);
