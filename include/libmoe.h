@@ -384,7 +384,8 @@ moe_status moe_page_plan(const int32_t* lens, const int32_t* new_tokens, int B, 
 
 /* The pages of ended sequences back to the pool: each sequence with ended[b] != 0 ([B] bytes) puts its pages on
  * the stack, sequences in order, and has length 0 afterwards; the page table stays as it is.  Lengths past the page table
- * are cut to it, and pages that the stack of n_pages entries has no room for are dropped; both record
+ * are cut to it, pages that the stack of n_pages entries has no room for are dropped, and an entry of the table outside
+ * [0, n_pages) goes on the stack as it is (a plan that comes to it gives no place there); each of these records
  * MOE_ERR_BAD_PAGE.  lens_out and n_free_out as above. */
 moe_status moe_page_release(const int32_t* lens, const uint8_t* ended, int B, const int32_t* page_table, int max_pages,
                             int32_t* free_pages, const int32_t* n_free, int n_pages, int page_size, int32_t* lens_out,

@@ -195,11 +195,14 @@ __global__ void __launch_bounds__(kTokenThreads) k_page_tokens(PlanArgs a) {
 
 // ---------------------------------------------------------------------------- release -------
 
-// Sequence b's pages, from place `at` of the stack on.
+// Sequence b's pages, from place `at` of the stack on.  What is no page of the pool goes there as well, so that the stack has
+// an entry for each that was taken (a plan gives no place in it), and is reported.
 __device__ __forceinline__ void give_back(const ReleaseArgs& a, int b, int at, int n, int lane, int lanes) {
   for (int j = lane; j < n; j += lanes) {
     const int64_t to = int64_t(at) + j;
-    if (to < a.n_pages) a.free_pages[to] = a.table[int64_t(b) * a.max_pages + j];
+    const int page = a.table[int64_t(b) * a.max_pages + j];
+    if (to < a.n_pages) a.free_pages[to] = page;
+    if (page < 0 || page >= a.n_pages) report_bad_page(reinterpret_cast<int*>(a.ws));
   }
 }
 
