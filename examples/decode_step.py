@@ -100,7 +100,9 @@ class Decoder:
 
 class Server(Decoder):
     """A Decoder whose sequences share a pool of pages and whose windowed layers turn queries and keys.  `lens` are the
-    tokens in the cache, and pos and slot those of the step's tokens, all on the device: admit() and step() plan them."""
+    tokens in the cache, and pos and slot those of the step's tokens, all on the device: admit() and step() plan them.
+    A row whose sequence was released is idle until a prompt is admitted to it: it has pos and slot -1, length 0 and no
+    pages, and its output means nothing."""
 
     def __init__(self, blocks, heads, kv_heads, dim, batch, width: int, rope: moe.Rope, alpha=0.5):
         table = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
@@ -110,17 +112,30 @@ class Server(Decoder):
         self.lens.zero_()
         self.free = torch.arange(self.n_pages, dtype=torch.int32, device="cuda")
         self.n_free = torch.full((1,), self.n_pages, dtype=torch.int32, device="cuda")
-        self.slot, self.seq = torch.empty_like(self.pos), torch.empty_like(self.pos)
+        # a plan's list has the tokens of busy rows one after the other (its parts 16-byte aligned)
+        self.places = torch.full((2, -(-batch // 4) * 4), -1, dtype=torch.int32, device="cuda")
+        self.rows = torch.full((2, batch), -1, dtype=torch.int32, device="cuda")
+        self.pos, self.slot = self.rows
+        self.seq = torch.empty(batch, dtype=torch.int32, device="cuda")
         self.starts = torch.empty(batch + 1, dtype=torch.int32, device="cuda")
+        self.busy = torch.ones(batch, dtype=torch.int32, device="cuda")  # tokens a step of each row
+        self.idle = torch.zeros(batch, dtype=torch.bool, device="cuda")
         self.plan_ws = moe.pages_workspace(batch)
 
     def admit(self, new_tokens: torch.Tensor, max_tokens: int) -> moe.PagePlan:
-        """Places for new_tokens[b] tokens of each sequence (the prompts')."""
-        return moe.page_plan(self.lens, new_tokens, self.page_table, self.free, self.n_free, self.page, self.n_pages,
+        """Places for new_tokens[b] tokens of each sequence (the prompts').  An idle row that gets some is busy."""
+        plan = moe.page_plan(self.lens, new_tokens, self.page_table, self.free, self.n_free, self.page, self.n_pages,
                              max_tokens, self.plan_ws)
+        self._idle(self.idle & ~((new_tokens > 0) & (self.lens > 0)))  # (one that found no pages has length 0)
+        return plan
 
     def release(self, ended: torch.Tensor):
         moe.page_release(self.lens, ended, self.page_table, self.free, self.n_free, self.page, self.plan_ws)
+        self._idle(self.idle | (ended != 0))
+
+    def _idle(self, rows: torch.Tensor):
+        self.idle.copy_(rows)
+        self.busy.copy_(~rows)
 
     def place(self, b, q, k, v):
         if b.window == 0:  # the layers of the whole context know no positions
@@ -128,8 +143,12 @@ class Server(Decoder):
         return moe.rope_kv_write(q, k, v, b.cache, self.rope, self.pos, self.slot, self.attn_ws, q_out=q)
 
     def step(self):
-        moe.page_plan(self.lens, None, self.page_table, self.free, self.n_free, self.page, self.n_pages, self.pos.shape[0],
-                      self.plan_ws, starts=self.starts, seq=self.seq, pos=self.pos, slot=self.slot)
+        batch = self.busy.shape[0]
+        moe.page_plan(self.lens, self.busy, self.page_table, self.free, self.n_free, self.page, self.n_pages, batch,
+                      self.plan_ws, starts=self.starts, seq=self.seq, pos=self.places[0, :batch], slot=self.places[1, :batch])
+        # from the list to the rows (a row without a token begins where the next one does, at its own number at most)
+        torch.index_select(self.places, 1, self.starts[:-1], out=self.rows)
+        self.rows.masked_fill_(self.idle, -1)
         return super().step()
 
     def advance(self):
