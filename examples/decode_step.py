@@ -191,23 +191,29 @@ def arguments(argv=None):
     return args
 
 
+PART = 1 << 16  # tokens that fill() writes at a time (a call of the library takes up to 2^20)
+
+
 def fill(dec: Decoder, context: int, start: int):
     """A context as if it had been decoded: random keys and values of every position."""
     h, hk, batch = dec.heads, dec.kv_heads, dec.residual.shape[0]
     serving = isinstance(dec, Server)
-    if serving:
-        plan = dec.admit(torch.full_like(dec.pos, start), batch * start)
-    for b in dec.blocks:
-        g = torch.Generator(device="cuda").manual_seed(7)
-        pos = torch.arange(start if serving else context, dtype=torch.int32, device="cuda")
-        for s in range(batch):
-            x = torch.randn(len(pos), h + 2 * hk, dec.dim, generator=g, device="cuda").bfloat16()
-            q, k, v = x[:, :h], x[:, h:h + hk], x[:, h + hk:]
-            if serving and b.window:
-                part = slice(s * start, (s + 1) * start)
-                moe.rope_kv_write(q, k, v, b.cache, dec.rope, plan.pos[part], plan.slot[part], dec.attn_ws, q_out=q)
-            else:
-                moe.kv_write(k, v, b.cache, pos, dec.page_table, dec.attn_ws, seq=torch.full_like(pos, s))
+    generators = [torch.Generator(device="cuda").manual_seed(7) for _ in dec.blocks]
+    n = start if serving else context
+    for s in range(batch):
+        for first in range(0, n, PART):
+            pos = torch.arange(first, min(n, first + PART), dtype=torch.int32, device="cuda")
+            if serving:
+                new = torch.zeros(batch, dtype=torch.int32, device="cuda")
+                new[s] = len(pos)
+                plan = dec.admit(new, len(pos))
+            for b, g in zip(dec.blocks, generators):
+                x = torch.randn(len(pos), h + 2 * hk, dec.dim, generator=g, device="cuda").bfloat16()
+                q, k, v = x[:, :h], x[:, h:h + hk], x[:, h + hk:]
+                if serving and b.window:
+                    moe.rope_kv_write(q, k, v, b.cache, dec.rope, plan.pos, plan.slot, dec.attn_ws, q_out=q)
+                else:
+                    moe.kv_write(k, v, b.cache, pos, dec.page_table, dec.attn_ws, seq=torch.full_like(pos, s))
 
 
 def main():
