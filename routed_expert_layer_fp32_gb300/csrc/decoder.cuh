@@ -212,11 +212,10 @@ struct NormArgs {
 };
 cudaError_t launch_block_norm(const NormArgs& a, cudaStream_t s);
 
-// Pages of new tokens (pages.cu).  Workspace: the status record, then a word (n_free before a release) and a word
-// a sequence and one more.
+// Pages of new tokens (pages.cu).  Workspace: the status record, then a word a sequence and one more.
 constexpr int kMaxPagePositions = 1 << 28;
 constexpr size_t kPagesWordsAt = sizeof(DevStatus);
-inline size_t pages_workspace_bytes(int B) { return align_up(kPagesWordsAt + (size_t(B) + 2) * 4, 256); }
+inline size_t pages_workspace_bytes(int B) { return align_up(kPagesWordsAt + (size_t(B) + 1) * 4, 256); }
 
 struct PlanArgs {
   const int32_t* lens;

@@ -4,11 +4,11 @@
 // what they address (the new tokens, or the pages given back).  The sums are one CTA's work, a run of sequences a
 // thread; the pass is the same CTA's where it is short, as in a decode step, else a second kernel's, a thread four
 // tokens or a CTA a sequence.  What bounds the calls is the chain lengths -> sums -> table -> places: a step of 64
-// sequences 3.3 us, 192 prompts with 342 thousand places 7.1 (4.9 MB: 0.7 at the copy rate), 64 of 256 sequences given
+// sequences 3.3 us, 192 prompts with 342 thousand places 7.3 (4.9 MB: 0.7 at the copy rate), 64 of 256 sequences given
 // back 4.7.  (Keeping the starts in shared memory for the search of a place's sequence changed nothing.)
 //
-// In place: the sums are done, and everything that comes from the lengths and n_free is written down, before either
-// is overwritten.  A new page's entry is written by the thread of its first token, and the stack itself is not written by a
+// In place: n_free is read by every thread before the sums' barriers and written behind them; a length is read and
+// written by one thread, which is done with it then.  A new page's entry is written by the thread of its first token, and the stack itself is not written by a
 // plan, so the second kernel needs no order among its CTAs.
 #include "decoder.cuh"
 
@@ -56,7 +56,7 @@ __device__ __forceinline__ int free_count(const int32_t* n_free, int n_pages, in
 // `first[b]`: where on the stack sequence b's first new page is; kRefused where its tokens have no place.
 constexpr int kRefused = -1;
 
-__device__ __forceinline__ int32_t* plan_first(const PlanArgs& a) { return reinterpret_cast<int32_t*>(a.ws + kPagesWordsAt) + 1; }
+__device__ __forceinline__ int32_t* plan_first(const PlanArgs& a) { return reinterpret_cast<int32_t*>(a.ws + kPagesWordsAt); }
 
 // Token t of the list: sequence b, its tokens from `start` on, the length it had before.
 __device__ __forceinline__ void place_token(const PlanArgs& a, int t, int b, int start, int before, int first, int& pos,
@@ -206,7 +206,7 @@ __device__ __forceinline__ void give_back(const ReleaseArgs& a, int b, int at, i
   }
 }
 
-// Workspace words: n_free before, then where each sequence's pages begin on the stack, and the end.
+// Workspace words: where each sequence's pages begin on the stack, and the end.
 template <bool kAll>
 __global__ void __launch_bounds__(kThreads) k_page_release(ReleaseArgs a) {
   __shared__ int64_t part[kThreads / 32];
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) k_page_release(ReleaseArgs a) {
   }
   // the places of all pages: those past the stack's end are one and the same, its end
   int64_t at = n_free + block_exclusive(mine, part, total);
-  int32_t* places = reinterpret_cast<int32_t*>(a.ws + kPagesWordsAt) + 1;
+  int32_t* places = reinterpret_cast<int32_t*>(a.ws + kPagesWordsAt);
   for (int b = b0; b < b1; ++b) {
     const int n = held(b), len = a.lens[b];
     places[b] = int(min(at, int64_t(a.n_pages)));
@@ -247,12 +247,12 @@ __global__ void __launch_bounds__(kThreads) k_page_release(ReleaseArgs a) {
 
 __global__ void __launch_bounds__(128) k_page_give_back(ReleaseArgs a) {
   pdl_begin();
-  const int32_t* places = reinterpret_cast<const int32_t*>(a.ws + kPagesWordsAt) + 1;
+  const int32_t* places = reinterpret_cast<const int32_t*>(a.ws + kPagesWordsAt);
   for (int b = blockIdx.x; b < a.B; b += gridDim.x)
     give_back(a, b, places[b], places[b + 1] - places[b], threadIdx.x, 128);
 }
 
-// Whole warps for as many sequences or tokens, up to kThreads: a small CTA starts and meets sooner (a step of 64: 3.6 -> 3.2
+// Whole warps for as many sequences or tokens, up to kThreads: a small CTA starts and meets sooner (a step of 64: 3.6 -> 3.3
 // us).
 int threads_for(int64_t n) { return int(std::min<int64_t>(kThreads, std::max<int64_t>(1, (n + 31) / 32) * 32)); }
 
