@@ -68,9 +68,8 @@ struct Partners {
   }
 };
 
-__device__ __forceinline__ void turn_of(const RopeDev& r, int pos, int e0, bool inverse, Turn& t) {
+__device__ __forceinline__ void turn_of(const RopeDev& r, int pos, int e0, Turn& t) {
   const int half = r.dim / 2;
-  const float sign = inverse ? -1.0f : 1.0f;
   if (r.interleaved) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
@@ -79,8 +78,8 @@ __device__ __forceinline__ void turn_of(const RopeDev& r, int pos, int e0, bool 
       if (e0 + i >= r.dim) continue;
       const float2 cs = cos_sin(__ldg(r.turns + (e0 + i) / 2), pos, r.magnitude);
       t.c[i] = t.c[i + 1] = cs.x;
-      t.s[i] = -sign * cs.y;
-      t.s[i + 1] = sign * cs.y;
+      t.s[i] = -cs.y;
+      t.s[i + 1] = cs.y;
     }
   } else {
 #pragma unroll
@@ -91,7 +90,7 @@ __device__ __forceinline__ void turn_of(const RopeDev& r, int pos, int e0, bool 
       if (e >= r.dim) continue;
       const float2 cs = cos_sin(__ldg(r.turns + (e < half ? e : e - half)), pos, r.magnitude);
       t.c[i] = cs.x;
-      t.s[i] = e < half ? -sign * cs.y : sign * cs.y;
+      t.s[i] = e < half ? -cs.y : cs.y;
     }
   }
 }
@@ -236,7 +235,7 @@ __device__ __forceinline__ void place_rows(const RopeArgs& a, int t, int lane, i
   Head<Src> next;
   load(j0, next);
   Turn turn;
-  if (j0 < a.k.heads) turn_of(a.rope, here ? a.pos[t] : 0, mine ? e0 : a.rope.dim, a.inverse, turn);
+  if (j0 < a.k.heads) turn_of(a.rope, here ? a.pos[t] : 0, mine ? e0 : a.rope.dim, turn);
   for (int j = j0; j < j1; ++j) {
     Head<Src> h = next;
     load(j + 1, next);
