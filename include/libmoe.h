@@ -366,12 +366,13 @@ size_t moe_pages_workspace_bytes(int B);
  *               n_free themselves)
  *   starts      [B + 1] int32: where each sequence's tokens begin on the list of all new tokens (in the order of
  *               sequences), cut to max_tokens
- *   seq, pos, slot  [max_tokens] int32: each new token's sequence and position, and its place in the cache,
- *               page * page_size + row; -1 in all three behind the last token
+ *   seq, pos, slot  [max_tokens] int32, 16-byte aligned: each new token's sequence and position, and its place in
+ *               the cache, page * page_size + row; -1 in all three behind the last token
  * A sequence that needs pages takes them from the top of the stack, sequences in order, and its entries of the
  * page table are written.  A sequence gets nothing if its tokens would go past its row of the page table or past
  * max_tokens, or if it needs pages and those of the sequences before it (served or not for want of pages) leave too
- * few: its tokens keep their place on the list with pos and slot -1 (moe_kv_write and moe_rope_kv_write skip those), its
+ * few (so one that is refused for want of pages holds up those behind it that need some: places are handed out in order):
+ * its tokens keep their place on the list with pos and slot -1 (moe_kv_write and moe_rope_kv_write skip those), its
  * length stays, and MOE_ERR_NO_PAGES is recorded.  A page outside [0, n_pages) in the table or in the pool gives
  * slots of -1, and an n_free outside [0, n_pages] counts as the nearest; both record MOE_ERR_BAD_PAGE.
  * B up to 65536, max_tokens up to 2^20, page_size 1 to 4096, max_pages * page_size up to 2^28, n_pages *
@@ -446,7 +447,7 @@ moe_status moe_rope_apply(const moe_rope_table* rope, const void* x, int64_t x_s
  *   q       rows of [n_heads, head_dim], k, v rows of [n_kv_heads, head_dim], bf16 or fp32 (dtype), q_stride,
  *           k_stride and v_stride elements apart (multiples of 16 bytes)
  *   q_out   bf16 rows of [n_heads, head_dim], q_out_stride elements apart: what moe_attn_decode takes (may be q, with its
- *           stride, where that is bf16; else apart from it)
+ *           stride, where that is bf16; else apart from it); apart from k, v and the cache
  *   pos     [T] int32: for the angles (a negative one too)
  *   slot    [T] int32: page * page_size + row of each token's place (moe_page_plan); negative: the key and value are
  *           not written.  A slot past the cache writes nothing and records MOE_ERR_BAD_PAGE in ws.  Two tokens of one call

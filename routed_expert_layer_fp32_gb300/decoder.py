@@ -282,8 +282,8 @@ def page_plan(lens: torch.Tensor, new_tokens: Optional[torch.Tensor], page_table
               pos: Optional[torch.Tensor] = None, slot: Optional[torch.Tensor] = None) -> PagePlan:
     """Room for new_tokens[b] (None: one) more tokens of each sequence, which has lens[b] in the cache: pages from the
     stack free_pages [n_pages], whose first n_free[0] entries are free, into page_table [B, max_pages], and the list of
-    all new tokens' sequences, positions and slots, padded to max_tokens.  lens and n_free are updated in place unless
-    lens_out and n_free_out are given."""
+    all new tokens' sequences, positions and slots, padded to max_tokens (seq, pos and slot, where they are given, begin at
+    a multiple of 16 bytes).  lens and n_free are updated in place unless lens_out and n_free_out are given."""
     (dev, B, width, table, lp, fp, n, np_, lens_out, lop, n_free_out, nop, wp, wn) = _pool(
         lens, page_table, free_pages, n_free, ws, lens_out, n_free_out)
     if n != n_pages:
