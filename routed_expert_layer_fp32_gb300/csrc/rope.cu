@@ -16,11 +16,11 @@
 // of the queries, then those of keys and values.
 //
 // Measured: 16k tokens of 32 heads of 128 bf16 turned 41.4 us, 97 % of the copy rate (with a row's eight elements a lane
-// and partners loaded for the queries too, one head ahead, 74.7); with 4 kv heads into a bf16 cache 59.7 us, 84 % (two or
-// four rows ahead 59.7 and 70.7, for their registers; two heads of keys and values a block 62.4); one token 2.0 us.  fp32 turned 79 us, the copy
-// rate.  16k tokens of 32 query and 4 kv heads, all of a head turned, halves paired: into a bf16 cache 61 us (82 % of the
-// copy rate), E4M3 70 (68 %), 4 bits 76 (62 %); from fp32 94, 93 and 95 (80, 78 and 75 %).  The kernels of quantised rows
-// take 73 and 74 registers, those of fp32 sources 102, which is three and two CTAs an SM, for the queries too.
+// and partners loaded for the queries too, one head ahead, 74.7), fp32 79 us, all of it; with 4 kv heads into a bf16 cache,
+// half of a head turned, 59.7 us, 84 % (two or four rows ahead 59.7 and 70.7, for their registers; two heads of keys and
+// values a block 62.4); one token 2.0 us.  All of a head turned, halves paired: into a bf16 cache 61 us (82 % of the copy
+// rate), E4M3 70 (68 %), 4 bits 76 (62 %); from fp32 94, 93 and 95 (80, 78 and 75 %).  The kernels of quantised rows take 73
+// and 74 registers, those of fp32 sources 102, which is three and two CTAs an SM, for the queries too.
 #include "kv_rows.cuh"
 
 namespace moe {
